@@ -80,6 +80,7 @@ typedef enum {
 #define PKV_DEV_ERR_BAD_BLOCK 2u /* decode: table entry outside [0, num_blocks), block skipped */
 #define PKV_DEV_ERR_BAD_LEN 4u   /* decode: seq_len < 0 or > max_blocks_per_seq * 16, clamped */
 #define PKV_DEV_ERR_TIMEOUT 8u   /* a bounded pipeline wait gave up */
+#define PKV_DEV_ERR_BAD_POS 16u  /* rotary write: position outside the table, token skipped */
 
 /* Directions of a block swap between the GPU cache and host swap space. */
 #define PKV_SWAP_OUT 0 /* GPU block -> host slot */
@@ -400,6 +401,129 @@ PKV_API pkv_status pkv_paged_attention_prefill(void *out, const void *q, const v
                                                int head_dim, int64_t num_blocks, float scale,
                                                unsigned int *err_word, void *stream);
 
+/*
+ * Rotary positions fused with the cache write: q and k are turned by their
+ * tokens' positions, q goes to q_out, k and v into the cache (the pages leave
+ * positions to the model; a token's cache slot says nothing of its position
+ * once tokens have been evicted, so positions are inputs).  Pair i, i in
+ * [0, rot_dim / 2), of a head is elements (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * when interleaved is 1; elements from rot_dim on are copied:
+ *   x1' = x1 cos - x2 sin,  x2' = x2 cos + x1 sin  (fp32, rounded to bf16 once)
+ *   cos, sin = cos_sin[P][i], cos_sin[P][rot_dim / 2 + i],  P = positions[pair_axis[i]][t]
+ * positions: device int32 [num_axes][num_tokens], 1 to PKV_ROPE_MAX_AXES axes
+ * (time, height, width, ...); pair_axis: HOST array [rot_dim / 2], the axis
+ * that turns each pair, read before the call returns (NULL: axis 0, allowed
+ * with one axis only).  cos_sin: device float [max_positions][rot_dim], the
+ * cosines of a position's pairs and then their sines (the caller's table:
+ * whatever base and scaling its model has).
+ * q, q_out: rows of num_heads x head_dim, k, v: rows of num_kv_heads x
+ * head_dim; *_stride: elements between tokens (at least a row, a multiple of
+ * 8), so slices of one projection's output need no copy.  q_out may be q itself
+ * (same pointer and stride); otherwise it must not overlap q, k or v.
+ * rot_dim: a multiple of 16, at most head_dim; head_dim 64 or 128.
+ * slot_mapping as for pkv_paged_kv_write: with a negative slot only q is
+ * turned; so too with a slot past the pool (PKV_DEV_ERR_BAD_SLOT).  A token
+ * with a position outside [0, max_positions) on any axis is left out whole
+ * (no q row, no cache write; PKV_DEV_ERR_BAD_POS).
+ */
+#define PKV_ROPE_MAX_AXES 4
+PKV_API pkv_status pkv_rope_kv_write(void *q_out, const void *q, const void *k, const void *v,
+                                     int64_t q_out_stride, int64_t q_stride, int64_t k_stride,
+                                     int64_t v_stride, void *k_cache, void *v_cache,
+                                     const int64_t *slot_mapping, const int32_t *positions,
+                                     int num_axes, const uint8_t *pair_axis, const float *cos_sin,
+                                     int64_t max_positions, int rot_dim, int interleaved,
+                                     int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                     int64_t num_blocks, unsigned int *err_word, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A cache that forgets: attention that also accumulates the weight each cached
+ * token gets, and the eviction of the tokens with the least.
+ *
+ * Scores: float [num_seqs][num_kv_heads][score_stride], score_stride >=
+ * max_blocks_per_seq * 16, row (b, g) entry p for the token at position p of
+ * sequence b's cache and KV head g (the sum over the head's query heads).
+ * scores_in is read at positions before the call's new tokens only, and
+ * scores_out is written at positions [0, seq_lens[b]) only, so neither needs
+ * clearing; scores_out may be scores_in itself (not a part of it at another
+ * offset); scores_in NULL stands for zeros.  Sums are fp32, taken in a fixed
+ * order: the same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pkv_paged_attention_decode_ex -- or, with k_new and v_new (both or neither),
+ * pkv_paged_decode_step -- that also gives
+ *   scores_out[b][g][p] = (p < seq_lens[b] - 1 ? scores_in[b][g][p] : 0)
+ *                         + sum over the query heads h of KV head g of softmax_p(scale q[b][h] . K_b)
+ * out and the cache have the bits of the call without scores with the same
+ * variant and partition.  Tokens of a block outside the pool get no weight.
+ * Workspace: pkv_decode_scored_workspace_bytes(...), else PKV_ERR_WORKSPACE.
+ */
+PKV_API size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                                 int head_dim, int max_blocks_per_seq,
+                                                 int partition_tokens);
+PKV_API pkv_status pkv_paged_attention_decode_scored(
+    void *out, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, int num_seqs,
+    int num_heads, int num_kv_heads, int head_dim, int64_t num_blocks, float scale,
+    const float *scores_in, float *scores_out, int64_t score_stride, int variant,
+    int partition_tokens, void *workspace, size_t workspace_bytes, unsigned int *err_word,
+    void *stream);
+
+/*
+ * pkv_paged_attention_prefill that also gives, for p in [0, seq_lens[b]),
+ *   scores_out[b][g][p] = (p < seq_lens[b] - rows_b ? scores_in[b][g][p] : 0)
+ *                         + sum over the last min(window, rows_b) new tokens at positions >= p, and
+ *                           the query heads h of KV head g, of their softmax weight on p
+ * (window <= 0: every new token counts).  num_tokens: the rows of q and out
+ * (query_start[num_seqs]).  scale > 0, at most 128 query heads per KV head.
+ * A sequence with seq_lens[b] < its rows, past its table, with more than
+ * max_query_len rows or rows past num_tokens is flagged PKV_DEV_ERR_BAD_LEN
+ * and its scores are not written; one without new tokens has its scores
+ * copied.  A table entry outside the pool is read as zeros
+ * (PKV_DEV_ERR_BAD_BLOCK).
+ * Workspace: pkv_prefill_scored_workspace_bytes(...) for the same sizes with
+ * the same device current, else PKV_ERR_WORKSPACE.
+ */
+PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_tokens, int num_seqs, int max_query_len,
+                                                  int num_heads, int num_kv_heads,
+                                                  int max_blocks_per_seq, int window);
+PKV_API pkv_status pkv_paged_attention_prefill_scored(
+    void *out, const void *q, int num_tokens, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+    const int32_t *query_start, int num_seqs, int max_query_len, int num_heads, int num_kv_heads,
+    int head_dim, int64_t num_blocks, float scale, const float *scores_in, float *scores_out,
+    int64_t score_stride, int window, void *workspace, size_t workspace_bytes,
+    unsigned int *err_word, void *stream);
+
+/*
+ * Eviction by accumulated weight.  For every sequence b and KV head g, of the
+ * tokens [0, seq_lens[b]) keep m = min(keep_lens[b], seq_lens[b]): the last
+ * r = min(recent, m), the first s = min(sink, m - r), and of the others the
+ * m - r - s with the highest scores_in[b][g] (equal scores: the lower
+ * position; NaN counts below everything).  Heads choose for themselves.  In
+ * position order, the i-th kept token's K and V rows go to position i of the
+ * sequence's new table, its score to scores_out[b][g][i] and its old position
+ * to kept[b][g][i]; entries from m on are not written.
+ * The old blocks are only read, so they may be shared with other sequences;
+ * no block of new_tables may appear in block_tables or twice in new_tables
+ * (pkv_alloc_evict gives such tables), and the two score arrays must not
+ * overlap.  scores_in [num_seqs][num_kv_heads][scores_in_stride >=
+ * max_blocks_per_seq * 16]; scores_out [..][scores_out_stride >=
+ * new_blocks_per_seq * 16]; kept int32 [..][new_blocks_per_seq * 16]; all device.
+ * Bad lengths (seq_lens[b] or keep_lens[b] negative or past their table) are
+ * clamped and flagged PKV_DEV_ERR_BAD_LEN; a row whose old or new block is
+ * outside the pool is not copied (PKV_DEV_ERR_BAD_BLOCK).
+ */
+PKV_API pkv_status pkv_evict_tokens(void *k_cache, void *v_cache, const int32_t *block_tables,
+                                    int max_blocks_per_seq, const int32_t *seq_lens,
+                                    const int32_t *new_tables, int new_blocks_per_seq,
+                                    const int32_t *keep_lens, const float *scores_in,
+                                    int64_t scores_in_stride, float *scores_out,
+                                    int64_t scores_out_stride, int32_t *kept, int sink, int recent,
+                                    int num_seqs, int num_kv_heads, int head_dim,
+                                    int64_t num_blocks, unsigned int *err_word, void *stream);
+
 /* ------------------------------------------------------------------------
  * Host block allocator (section 二 and section 三 of the first page): a pool
  * of num_blocks physical blocks with reference counts, per-sequence block
@@ -481,6 +605,17 @@ PKV_API pkv_status pkv_alloc_swap_in(pkv_alloc *a, int64_t seq_id);
  * again, swap-ins before the sequence is decoded. */
 PKV_API pkv_status pkv_alloc_take_swaps(pkv_alloc *a, int direction, int64_t *gpu_out,
                                         int64_t *host_out, int64_t cap, int64_t *n_out);
+
+/* Shrinks n distinct sequences to keep_tokens[i] in [0, their length] tokens
+ * each, in fresh blocks (for pkv_evict_tokens: export the old tables, call
+ * this, export the new ones): every fresh block is taken before any old one
+ * returns to the pool, so that no old block of the call is a new one; all or
+ * none (PKV_ERR_OOM when the free blocks do not hold the kept tokens: evict
+ * fewer sequences at a time).  Old blocks that other tables hold stay theirs.
+ * The eviction must be ordered on the GPU before the next writes into the
+ * returned blocks, and after queued copies (pkv_alloc_take_copies). */
+PKV_API pkv_status pkv_alloc_evict(pkv_alloc *a, const int64_t *seq_ids, int n,
+                                   const int64_t *keep_tokens);
 
 /* Release a sequence: every block whose count drops to zero returns to the pool. */
 PKV_API pkv_status pkv_alloc_free_seq(pkv_alloc *a, int64_t seq_id);

@@ -160,6 +160,28 @@ class BlockManager:
                     self.free.append(b)
         del self.lens[seq_id]
 
+    def evict(self, seq_ids, keep_tokens) -> None:
+        """Each listed sequence shrunk to keep_tokens[i] tokens in fresh
+        blocks, all or none: every fresh block is taken (in list order) before
+        any old one returns to the pool."""
+        ids, keep = list(seq_ids), [int(k) for k in keep_tokens]
+        if len(set(ids)) != len(ids) or any(s not in self.tables or s in self.swapped for s in ids) \
+                or any(not 0 <= k <= self.lens[s] for s, k in zip(ids, keep)):
+            raise AllocError("invalid", "unknown or repeated sequence, or more tokens than it has")
+        if sum(blocks_for(k) for k in keep) > len(self.free):
+            raise AllocError("oom")
+        old = [self.tables[s] for s in ids]
+        for s, k in zip(ids, keep):
+            self.tables[s] = [self.free.popleft() for _ in range(blocks_for(k))]
+            self.lens[s] = k
+            for b in self.tables[s]:
+                self.ref[b] = 1
+        for blocks in old:
+            for b in blocks:
+                self.ref[b] -= 1
+                if self.ref[b] == 0:
+                    self.free.append(b)
+
     def set_host_pool(self, n: int) -> None:
         if n < 0 or self.swapped:
             raise AllocError("invalid", "bad size or host slots in use")

@@ -330,6 +330,49 @@ pkv_status pkv_alloc_free_seq(pkv_alloc *a, int64_t seq_id) {
     return PKV_OK;
 }
 
+pkv_status pkv_alloc_evict(pkv_alloc *a, const int64_t *seq_ids, int n, const int64_t *keep_tokens) {
+    if (!a || n < 0 || (n > 0 && (!seq_ids || !keep_tokens))) return PKV_ERR_INVALID_ARG;
+    const uint64_t epoch = ++a->epoch;
+    std::vector<std::vector<int32_t>> fresh;
+    std::vector<Sequence *> seqs;
+    try {
+        size_t need = 0;
+        fresh.resize(static_cast<size_t>(n));
+        seqs.reserve(static_cast<size_t>(n));
+        for (int i = 0; i < n; ++i) {
+            auto it = a->seqs.find(seq_ids[i]);
+            if (it == a->seqs.end() || it->second.swapped) return PKV_ERR_INVALID_ARG;
+            Sequence &s = it->second;
+            if (s.mark == epoch || keep_tokens[i] < 0 || keep_tokens[i] > s.len) return PKV_ERR_INVALID_ARG;
+            s.mark = epoch;
+            const size_t blocks = static_cast<size_t>(blocks_for(keep_tokens[i]));
+            fresh[static_cast<size_t>(i)].reserve(blocks);
+            need += blocks;
+            seqs.push_back(&s);
+        }
+        if (need > a->free_list.size()) return PKV_ERR_OOM;
+    } catch (const std::bad_alloc &) {
+        return PKV_ERR_OOM;
+    }
+    // every fresh block is taken before an old one is returned
+    for (int i = 0; i < n; ++i) {
+        std::vector<int32_t> &f = fresh[static_cast<size_t>(i)];
+        for (int64_t j = blocks_for(keep_tokens[i]); j > 0; --j) {
+            f.push_back(a->free_list.front());
+            a->free_list.pop_front();
+            a->refcount[f.back()] = 1;
+        }
+    }
+    for (int i = 0; i < n; ++i) {
+        Sequence &s = *seqs[static_cast<size_t>(i)];
+        s.blocks.swap(fresh[static_cast<size_t>(i)]);
+        s.len = keep_tokens[i];
+        for (int32_t b : fresh[static_cast<size_t>(i)])
+            if (--a->refcount[b] == 0) a->free_list.push_back(b);
+    }
+    return PKV_OK;
+}
+
 pkv_status pkv_alloc_set_host_pool(pkv_alloc *a, int64_t num_host_blocks) {
     if (!a || num_host_blocks < 0 || num_host_blocks > INT32_MAX) return PKV_ERR_INVALID_ARG;
     for (const auto &kv : a->seqs)

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(D) splitk_merge_kernel(const DecodeParams p) {
             }
         }
         p.out[row * D + e] = __float2bfloat16(L > 0.f ? O / L : 0.f);
+        if (p.lse != nullptr && e == 0) p.lse[row] = M + log2f(L);
         return;
     }
     // M over all partitions
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(D) splitk_merge_kernel(const DecodeParams p) {
         for (; q < n; ++q) O = fmaf(ob[static_cast<size_t>(q) * D], s_w[q], O);
     }
     p.out[row * D + e] = __float2bfloat16(L > 0.f ? O / L : 0.f);
+    if (p.lse != nullptr && e == 0) p.lse[row] = M + log2f(L);
 }
 
 template <int D, int NW, int S, bool MMA, int MODE>
@@ -280,6 +282,13 @@ cudaError_t launch_order(const int32_t *seq_lens, int B, int W, int32_t *order, 
     while ((W >> shift) >= kOrderBuckets) ++shift;
     return launch_dependent(order_kernel, dim3(1), dim3(kOrderThreads), stream, seq_lens, B, W, shift,
                             order);
+}
+
+cudaError_t launch_splitk_merge(const DecodeParams &p, int head_dim, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(p.Hq), static_cast<unsigned>(p.B));
+    if (head_dim == 128) return launch_dependent(splitk_merge_kernel<128>, grid, dim3(128), stream, p);
+    if (head_dim == 64) return launch_dependent(splitk_merge_kernel<64>, grid, dim3(64), stream, p);
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_decode(const CUtensorMap &tmk, const CUtensorMap &tmv, const DecodeParams &p,

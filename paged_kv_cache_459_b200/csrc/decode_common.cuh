@@ -126,7 +126,11 @@ struct ScalarHead {
         l_run = 0.f;
     }
 
-    __device__ __forceinline__ void tile(const uint8_t *kt, const uint8_t *vt, int nvalid, int lane) {
+    // With LOGITS the tile's scores (log2 domain) also go to logits[row], rows
+    // in [0, nvalid).
+    template <bool LOGITS = false>
+    __device__ __forceinline__ void tile(const uint8_t *kt, const uint8_t *vt, int nvalid, int lane,
+                                         float *logits = nullptr) {
         float acc[RPL];
 #pragma unroll
         for (int j = 0; j < RPL; ++j) {
@@ -156,6 +160,9 @@ struct ScalarHead {
         }
         float s = acc[0] + __shfl_xor_sync(0xffffffffu, acc[0], 1);
         const int my_row = g + RG * ((lane % CH) >> 1);
+        if constexpr (LOGITS) {
+            if (my_row < nvalid && !(lane & 1)) logits[my_row] = s;
+        }
         if (my_row >= nvalid) s = -INFINITY;
         float mx = s;
 #pragma unroll
@@ -239,7 +246,11 @@ struct GroupHeads {
         scale_log2 = sl2;
     }
 
-    __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int nvalid, int lane) {
+    // With LOGITS the tile's scores (log2 domain) also go to
+    // logits[row * width + head], rows in [0, nvalid), heads in [0, width), width even.
+    template <bool LOGITS = false>
+    __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int nvalid, int lane,
+                                         float *logits = nullptr, int width = 0) {
         const int tig = lane & 3, gid = lane >> 2;
         float sc[4] = {0.f, 0.f, 0.f, 0.f};
         {
@@ -255,6 +266,14 @@ struct GroupHeads {
         // sc: [token gid][head 2tig], [gid][2tig+1], [gid+8][2tig], [gid+8][2tig+1]
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i] *= scale_log2;
+        if constexpr (LOGITS) {
+            if (2 * tig < width) {
+                if (gid < nvalid)
+                    *reinterpret_cast<float2 *>(logits + gid * width + 2 * tig) = make_float2(sc[0], sc[1]);
+                if (gid + 8 < nvalid)
+                    *reinterpret_cast<float2 *>(logits + (gid + 8) * width + 2 * tig) = make_float2(sc[2], sc[3]);
+            }
+        }
         if (gid >= nvalid) sc[0] = sc[1] = -INFINITY;
         if (gid + 8 >= nvalid) sc[2] = sc[3] = -INFINITY;
         float mx0 = fmaxf(sc[0], sc[2]), mx1 = fmaxf(sc[1], sc[3]);

@@ -37,7 +37,9 @@ constexpr int cluster_land_bytes() {
 // One work unit (partition `part` of sequence b, KV head / head chunk `by`)
 // of the per-unit decode kernel, run by a CTA of NW warps.  The warps take
 // the unit's blocks round-robin and are combined in shared memory at the end.
-template <int D, int NW, int S, bool MMA, int MODE>
+// With SCORED the unit also leaves its tokens' scores in p.logits and, where
+// it finishes a row, the row's log-sum-exp in p.lse (both log2 domain).
+template <int D, int NW, int S, bool MMA, int MODE, bool SCORED = false>
 __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtensorMap &tmv,
                                             const DecodeParams &p, int part, int by, int b,
                                             bool wait_pending = false) {
@@ -213,6 +215,12 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
         issue(i);
     }
 
+    // logits: [sequence][KV head][chunk of heads][token][logit_width]
+    float *logits = nullptr;
+    if constexpr (SCORED)
+        logits = p.logits + ((static_cast<size_t>(b) * p.Hkv + kvh) * p.chunks + chunk) *
+                                static_cast<size_t>(p.W) * kBlockTokens * p.logit_width;
+
     int i = 0;
     for (; i < n_mine; ++i) {
         tw.advance_to(i, lane);
@@ -226,10 +234,18 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
             const int lb = blk_begin + lead + kStride * i;
             const int nvalid = min(kBlockTokens, len - lb * kBlockTokens);
             const uint8_t *kt = ring + s * G::kStageBytes;
-            if constexpr (MMA)
+            if constexpr (SCORED) {
+                float *lg = logits + static_cast<size_t>(lb) * kBlockTokens * p.logit_width;
+                if constexpr (MMA)
+                    st.template tile<true>(smem_u32(kt), smem_u32(kt + G::kTileBytes), nvalid, lane, lg,
+                                           p.logit_width);
+                else
+                    st.template tile<true>(kt, kt + G::kTileBytes, nvalid, lane, lg);
+            } else if constexpr (MMA) {
                 st.tile(smem_u32(kt), smem_u32(kt + G::kTileBytes), nvalid, lane);
-            else
+            } else {
                 st.tile(kt, kt + G::kTileBytes, nvalid, lane);
+            }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -317,6 +333,9 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
             }
         } else {
             p.out[row * D + e] = __float2bfloat16(L > 0.f ? O / L : 0.f);
+            if constexpr (SCORED) {
+                if (e == 0) p.lse[row] = M + log2f(L);
+            }
         }
     }
     if constexpr (CLUSTER) {
@@ -368,6 +387,9 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
             }
             p.out[(static_cast<size_t>(b) * p.Hq + h0 + n) * D + e] =
                 __float2bfloat16(L > 0.f ? O / L : 0.f);
+            if constexpr (SCORED) {
+                if (e == 0) p.lse[static_cast<size_t>(b) * p.Hq + h0 + n] = M + log2f(L);
+            }
         }
     }
 }

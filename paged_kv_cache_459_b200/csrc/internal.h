@@ -48,6 +48,10 @@ struct DecodeParams {
     // into the slot of position len - 1 before that unit reads the block.
     const __nv_bfloat16 *k_new, *v_new;
     __nv_bfloat16 *k_cache, *v_cache;  // [num_blocks][Hkv][16][D], for those stores
+    // Scored decode only (log2 domain): every token's score
+    // [B][Hkv][chunks][W * 16][logit_width] and each row's log-sum-exp [B][Hq].
+    float *logits, *lse;
+    int logit_width;  // heads of a chunk, rounded up to even where there is a group
 };
 
 // Longest-first order of the sequences (by block count) into order[B], for
@@ -69,6 +73,19 @@ constexpr int kMaxClusterParts = 8;
 // the order kernel and waits for it.
 cudaError_t launch_decode(const CUtensorMap &tmk, const CUtensorMap &tmv, const DecodeParams &p,
                           int head_dim, int mode, DecodeTuning tuning, cudaStream_t stream);
+
+// The split-K merge alone (of partials that another launch left in p's workspace).
+cudaError_t launch_splitk_merge(const DecodeParams &p, int head_dim, cudaStream_t stream);
+
+// Scored decode: launch_decode with p.logits and p.lse written, then the
+// tokens' weights, summed over each KV head's query heads, added to scores.
+struct ScoreParams {
+    const float *scores_in;  // [B][Hkv][stride], nullable (zeros)
+    float *scores_out;       // the same layout; may be scores_in itself
+    long long stride;
+};
+cudaError_t launch_decode_scored(const CUtensorMap &tmk, const CUtensorMap &tmv, const DecodeParams &p,
+                                 const ScoreParams &sp, int head_dim, int mode, cudaStream_t stream);
 
 // Shared-prefix (cascade) decode: prefix blocks read once per (group, KV
 // head) by a dense tensor-core kernel; suffixes by split-K; LSE merge.
@@ -110,6 +127,10 @@ struct PrefillParams {
     long long num_blocks;
     int W, B, Hq, Hkv, group;
     float scale_log2;
+    // Optional: each row's log-sum-exp (log2 domain), rows of one KV head
+    // together: lse[(kv head * num_tokens + token) * group + head of the group].
+    float *lse;
+    int num_tokens;  // tokens of q that lse has room for
     int items;  // work items of the persistent tcgen05 kernel (set by its launcher)
 };
 
@@ -117,6 +138,53 @@ struct PrefillParams {
 // 128-row Q tiles.
 cudaError_t launch_prefill_tc(const CUtensorMap &tmk, const CUtensorMap &tmv, const PrefillParams &p,
                               int head_dim, int max_query_len, int num_sms, cudaStream_t stream);
+
+// The weights that the last `window` new tokens of each sequence put on its
+// tokens, from the prefill's log-sum-exp (pp.lse), added to the scores.
+struct PrefillScoreParams {
+    PrefillParams pp;
+    ScoreParams sp;
+    float *partial;     // [splits][B][Hkv][W * 16] when splits > 1
+    int splits;         // row ranges a key tile's queries are cut into
+    int window;         // new tokens counted (INT_MAX: all)
+    int max_query_len;
+    int tile_tokens;    // tokens of a 128-row query tile (128 / group)
+};
+cudaError_t launch_prefill_scores(const CUtensorMap &tmk, const CUtensorMap &tmq,
+                                  const PrefillScoreParams &p, int head_dim, cudaStream_t stream);
+// The splits launch_prefill_scores cuts these sizes into (its workspace depends on it).
+int prefill_score_splits(int B, int Hkv, int group, int W, int window, int max_query_len, int num_sms);
+
+// Rotary positions of q and k, q to q_out, k and v into the cache.
+struct RopeParams {
+    __nv_bfloat16 *q_out;
+    const __nv_bfloat16 *q, *k, *v;
+    long long q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
+    __nv_bfloat16 *k_cache, *v_cache;
+    const int64_t *slots;      // [T]
+    const int32_t *positions;  // [axes][T]
+    const float *cos_sin;      // [max_positions][rot]: cosines of the pairs, then their sines
+    long long max_positions, num_blocks;
+    unsigned int *err;
+    int T, Hq, Hkv, rot, axes;
+    uint32_t axis_bits[8];     // two bits of axis for each pair, 8 pairs a half word
+};
+cudaError_t launch_rope_kv_write(const RopeParams &p, int head_dim, bool interleaved, int num_sms,
+                                 cudaStream_t stream);
+
+// Eviction: each (sequence, KV head)'s kept tokens into fresh blocks.
+struct EvictParams {
+    __nv_bfloat16 *k_cache, *v_cache;
+    const int32_t *block_tables, *seq_lens;  // [B][W], [B]
+    const int32_t *new_tables, *keep_lens;   // [B][NW], [B]
+    const float *scores_in;                  // [B][Hkv][in_stride]
+    float *scores_out;                       // [B][Hkv][out_stride]
+    int32_t *kept;                           // [B][Hkv][NW * 16]
+    long long in_stride, out_stride, num_blocks;
+    unsigned int *err;
+    int W, NW, B, Hkv, sink, recent;
+};
+cudaError_t launch_evict(const EvictParams &p, int head_dim, cudaStream_t stream);
 
 cudaError_t launch_copy_blocks(void *k_cache, void *v_cache, const int64_t *src, const int64_t *dst,
                                int n, int num_kv_heads, int head_dim, long long num_blocks,

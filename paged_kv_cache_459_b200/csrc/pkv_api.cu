@@ -17,6 +17,8 @@ constexpr int kDefaultPartitionTokens = 512;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -291,13 +293,39 @@ int pkv_decode_cluster_parts_for(int num_seqs, int num_heads, int num_kv_heads, 
     return plan.variant == PKV_DECODE_CLUSTER ? plan.parts : 0;
 }
 
+namespace {
+
+// Heads of a chunk of the scored decode's logits, rounded up to even.
+int logit_width(int group) { return group == 1 ? 1 : (std::min(group, 8) + 1) / 2 * 2; }
+
+// The scored decode's workspace: what the decode may use, then the tokens'
+// scores, then the rows' log-sum-exp (byte offsets, 256-byte aligned).
+struct ScoredWorkspace {
+    size_t logits, lse, total;
+};
+ScoredWorkspace scored_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq, int partition_tokens) {
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const int group = num_heads / num_kv_heads, chunks = (group + 7) / 8;
+    ScoredWorkspace w;
+    w.logits = up(pkv_decode_workspace_bytes_for(PKV_DECODE_AUTO, num_seqs, num_heads, num_kv_heads,
+                                                 head_dim, max_blocks_per_seq, partition_tokens));
+    w.lse = w.logits + up(static_cast<size_t>(num_seqs) * num_kv_heads * chunks * logit_width(group) *
+                          (static_cast<size_t>(max_blocks_per_seq) * PKV_BLOCK_TOKENS) * sizeof(float));
+    w.total = w.lse + up(static_cast<size_t>(num_seqs) * num_heads * sizeof(float));
+    return w;
+}
+
+}  // namespace
+
 static pkv_status decode_impl(void *out, const void *q, const void *k_cache, const void *v_cache,
                               const int32_t *block_tables, int max_blocks_per_seq,
                               const int32_t *seq_lens, int num_seqs, int num_heads,
                               int num_kv_heads, int head_dim, int64_t num_blocks, float scale,
                               int variant, int partition_tokens, void *workspace,
                               size_t workspace_bytes, unsigned int *err_word, void *stream,
-                              const void *k_new, const void *v_new) {
+                              const void *k_new, const void *v_new,
+                              const pkv::ScoreParams *scores = nullptr) {
     if (num_seqs < 0 || num_seqs > 65535 || num_heads <= 0 || num_kv_heads <= 0 ||
         num_heads % num_kv_heads || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
         !std::isfinite(scale))
@@ -319,7 +347,18 @@ static pkv_status decode_impl(void *out, const void *q, const void *k_cache, con
 
     const int part_blocks = partition_tokens / PKV_BLOCK_TOKENS;
     const bool ws_aligned = workspace != nullptr && aligned16(workspace);
-    const size_t have = ws_aligned ? workspace_bytes : 0;
+    size_t have = ws_aligned ? workspace_bytes : 0;
+    ScoredWorkspace sw{};
+    if (scores != nullptr) {
+        if (scores->stride < static_cast<int64_t>(max_blocks_per_seq) * PKV_BLOCK_TOKENS ||
+            num_kv_heads > 65535 || !scores->scores_out || !aligned4(scores->scores_out) ||
+            !aligned4(scores->scores_in))
+            return PKV_ERR_INVALID_ARG;
+        sw = scored_workspace(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                              partition_tokens);
+        if (have < sw.total) return PKV_ERR_WORKSPACE;
+        have = sw.logits;  // what the decode itself may use
+    }
     const size_t split_bytes = pkv_decode_workspace_bytes(num_seqs, num_heads, head_dim,
                                                           max_blocks_per_seq, partition_tokens);
     DecodePlan plan{variant, 1};
@@ -375,6 +414,11 @@ static pkv_status decode_impl(void *out, const void *q, const void *k_cache, con
         // longest sequences first, when the workspace has room for the order
         use_order = have >= static_cast<size_t>(num_seqs) * sizeof(int32_t);
     }
+    if (scores != nullptr) {
+        p.logits = reinterpret_cast<float *>(static_cast<char *>(workspace) + sw.logits);
+        p.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + sw.lse);
+        p.logit_width = logit_width(p.group);
+    }
     if (use_order) {
         int32_t *order = static_cast<int32_t *>(workspace);
         cudaError_t e = pkv::launch_order(seq_lens, num_seqs, max_blocks_per_seq, order,
@@ -382,6 +426,9 @@ static pkv_status decode_impl(void *out, const void *q, const void *k_cache, con
         if (e != cudaSuccess) return cuda_status(e);
         p.order = order;
     }
+    if (scores != nullptr)
+        return cuda_status(pkv::launch_decode_scored(tmk, tmv, p, *scores, head_dim, mode,
+                                                     static_cast<cudaStream_t>(stream)));
     pkv::DecodeTuning t{env_int("PKV_DECODE_WARPS", 4), env_int("PKV_DECODE_STAGES", 2)};
     cudaError_t e = pkv::launch_decode(tmk, tmv, p, head_dim, mode, t,
                                        static_cast<cudaStream_t>(stream));
@@ -415,6 +462,33 @@ pkv_status pkv_paged_decode_step(void *out, const void *q, const void *k_new, co
                        num_seqs, num_heads, num_kv_heads, head_dim, num_blocks, scale, variant,
                        partition_tokens, workspace, workspace_bytes, err_word, stream, k_new,
                        v_new);
+}
+
+size_t pkv_decode_scored_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                         int max_blocks_per_seq, int partition_tokens) {
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
+        head_dim <= 0 || max_blocks_per_seq <= 0)
+        return 0;
+    if (partition_tokens <= 0) partition_tokens = kDefaultPartitionTokens;
+    if (partition_tokens % PKV_BLOCK_TOKENS) return 0;
+    return scored_workspace(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                            partition_tokens).total;
+}
+
+pkv_status pkv_paged_attention_decode_scored(
+    void *out, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, int num_seqs,
+    int num_heads, int num_kv_heads, int head_dim, int64_t num_blocks, float scale,
+    const float *scores_in, float *scores_out, int64_t score_stride, int variant,
+    int partition_tokens, void *workspace, size_t workspace_bytes, unsigned int *err_word,
+    void *stream) {
+    if ((k_new == nullptr) != (v_new == nullptr) || !aligned16(k_new) || !aligned16(v_new))
+        return PKV_ERR_INVALID_ARG;
+    const pkv::ScoreParams sp{scores_in, scores_out, score_stride};
+    return decode_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                       num_seqs, num_heads, num_kv_heads, head_dim, num_blocks, scale, variant,
+                       partition_tokens, workspace, workspace_bytes, err_word, stream, k_new, v_new,
+                       &sp);
 }
 
 size_t pkv_decode_prefix_workspace_bytes(int num_seqs, int num_heads, int head_dim,
@@ -612,6 +686,241 @@ pkv_status pkv_paged_attention_prefill(void *out, const void *q, const void *k_c
     cudaError_t e = pkv::launch_prefill_tc(tmk, tmv, p, head_dim, max_query_len, sm_count(),
                                            static_cast<cudaStream_t>(stream));
     return cuda_status(e);
+}
+
+namespace {
+
+// The prefill scores' workspace: the rows' log-sum-exp, then the partial sums
+// when each unit's queries are cut into ranges.
+struct PrefillScoreWorkspace {
+    size_t partial, total;
+    int splits;
+};
+PrefillScoreWorkspace prefill_score_workspace(int num_tokens, int num_seqs, int max_query_len,
+                                              int num_heads, int num_kv_heads,
+                                              int max_blocks_per_seq, int window) {
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    PrefillScoreWorkspace w;
+    w.splits = pkv::prefill_score_splits(num_seqs, num_kv_heads, num_heads / num_kv_heads,
+                                         max_blocks_per_seq, window, max_query_len, sm_count());
+    w.partial = up(static_cast<size_t>(num_tokens) * num_heads * sizeof(float));
+    w.total = w.partial;
+    if (w.splits > 1)
+        w.total += up(static_cast<size_t>(w.splits) * num_seqs * num_kv_heads *
+                      (static_cast<size_t>(max_blocks_per_seq) * PKV_BLOCK_TOKENS) * sizeof(float));
+    return w;
+}
+
+int window_or_all(int window) { return window > 0 ? window : INT32_MAX; }
+
+// q [T][Hq][d] as TMA sees it for the prefill scores: boxes of [tokens]
+// [heads of a group][64 columns].
+bool encode_q_map(CUtensorMap *m, const void *q, int num_tokens, int num_heads, int head_dim,
+                  int group, int tile_tokens) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_heads),
+                          static_cast<cuuint64_t>(num_tokens)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                             static_cast<cuuint64_t>(num_heads) * head_dim * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tile_tokens)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
+                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t pkv_prefill_scored_workspace_bytes(int num_tokens, int num_seqs, int max_query_len,
+                                          int num_heads, int num_kv_heads, int max_blocks_per_seq,
+                                          int window) {
+    if (num_tokens < 0 || num_seqs < 0 || max_query_len < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        num_heads % num_kv_heads || max_blocks_per_seq <= 0)
+        return 0;
+    return prefill_score_workspace(num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads,
+                                   max_blocks_per_seq, window_or_all(window)).total;
+}
+
+pkv_status pkv_paged_attention_prefill_scored(
+    void *out, const void *q, int num_tokens, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+    const int32_t *query_start, int num_seqs, int max_query_len, int num_heads, int num_kv_heads,
+    int head_dim, int64_t num_blocks, float scale, const float *scores_in, float *scores_out,
+    int64_t score_stride, int window, void *workspace, size_t workspace_bytes,
+    unsigned int *err_word, void *stream) {
+    if (num_tokens < 0 || num_seqs < 0 || num_seqs > 65535 || max_query_len < 0 || num_heads <= 0 ||
+        num_kv_heads <= 0 || num_kv_heads > 65535 || num_heads % num_kv_heads ||
+        max_blocks_per_seq <= 0 || num_blocks <= 0 || !std::isfinite(scale) || !(scale > 0.f))
+        return PKV_ERR_INVALID_ARG;
+    const int group = num_heads / num_kv_heads;
+    if ((head_dim != 64 && head_dim != 128) || group > 128) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_tables || !seq_lens || !query_start || !scores_out ||
+        (num_tokens > 0 && (!out || !q)))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned4(scores_in) || !aligned4(scores_out))
+        return PKV_ERR_INVALID_ARG;
+    if (num_blocks > INT32_MAX / PKV_BLOCK_TOKENS / num_kv_heads) return PKV_ERR_UNSUPPORTED;
+    const int64_t row_tokens = static_cast<int64_t>(max_blocks_per_seq) * PKV_BLOCK_TOKENS;
+    if (row_tokens > 65535 * 128) return PKV_ERR_UNSUPPORTED;  // key tiles of a launch
+    if (score_stride < row_tokens) return PKV_ERR_INVALID_ARG;
+    const int counted = window_or_all(window);
+    const PrefillScoreWorkspace sw = prefill_score_workspace(
+        num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads, max_blocks_per_seq, counted);
+    if (sw.total > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < sw.total))
+        return PKV_ERR_WORKSPACE;
+
+    const int64_t rows = num_blocks * num_kv_heads * PKV_BLOCK_TOKENS;
+    CUtensorMap tmk, tmv, tmk_scores, tmq;
+    pkv::PrefillScoreParams p{};
+    p.pp.out = static_cast<__nv_bfloat16 *>(out);
+    p.pp.q = static_cast<const __nv_bfloat16 *>(q);
+    p.pp.block_tables = block_tables;
+    p.pp.seq_lens = seq_lens;
+    p.pp.query_start = query_start;
+    p.pp.err = err_word;
+    p.pp.num_blocks = num_blocks;
+    p.pp.W = max_blocks_per_seq;
+    p.pp.B = num_seqs;
+    p.pp.Hq = num_heads;
+    p.pp.Hkv = num_kv_heads;
+    p.pp.group = group;
+    p.pp.scale_log2 = scale * 1.4426950408889634f;
+    p.pp.lse = static_cast<float *>(workspace);
+    p.pp.num_tokens = num_tokens;
+    p.sp = pkv::ScoreParams{scores_in, scores_out, score_stride};
+    p.splits = sw.splits;
+    p.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + sw.partial);
+    p.window = counted;
+    p.max_query_len = num_tokens > 0 ? max_query_len : 0;
+    p.tile_tokens = 128 / group;
+    if (!encode_cache_map(&tmk, k_cache, rows, head_dim) ||
+        !encode_cache_map(&tmv, v_cache, rows, head_dim))
+        return PKV_ERR_CUDA;
+    tmk_scores = tmk;
+    // without new tokens there is no q: no unit loads a query tile
+    tmq = tmk;
+    if (num_tokens > 0 && !encode_q_map(&tmq, q, num_tokens, num_heads, head_dim, group, p.tile_tokens))
+        return PKV_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.max_query_len > 0) {
+        const cudaError_t e =
+            pkv::launch_prefill_tc(tmk, tmv, p.pp, head_dim, p.max_query_len, sm_count(), s);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    return cuda_status(pkv::launch_prefill_scores(tmk_scores, tmq, p, head_dim, s));
+}
+
+pkv_status pkv_rope_kv_write(void *q_out, const void *q, const void *k, const void *v,
+                             int64_t q_out_stride, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, void *k_cache, void *v_cache,
+                             const int64_t *slot_mapping, const int32_t *positions, int num_axes,
+                             const uint8_t *pair_axis, const float *cos_sin, int64_t max_positions,
+                             int rot_dim, int interleaved, int num_tokens, int num_heads,
+                             int num_kv_heads, int head_dim, int64_t num_blocks,
+                             unsigned int *err_word, void *stream) {
+    if (num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+        max_positions <= 0 || num_axes < 1 || num_axes > PKV_ROPE_MAX_AXES ||
+        (num_axes > 1 && !pair_axis) || (interleaved != 0 && interleaved != 1))
+        return PKV_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (rot_dim <= 0 || rot_dim > head_dim || rot_dim % 16) return PKV_ERR_INVALID_ARG;
+    if (num_heads > INT32_MAX / 4 / head_dim || num_kv_heads > INT32_MAX / 4 / head_dim)
+        return PKV_ERR_INVALID_ARG;
+    const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim;
+    const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (q_out_stride < q_row || q_stride < q_row || k_stride < kv_row || v_stride < kv_row ||
+        q_out_stride % 8 || q_stride % 8 || k_stride % 8 || v_stride % 8)
+        return PKV_ERR_INVALID_ARG;
+    if (num_blocks > (INT64_MAX / PKV_BLOCK_TOKENS) / num_kv_heads / head_dim ||
+        max_positions > INT64_MAX / 4 / rot_dim)
+        return PKV_ERR_INVALID_ARG;
+    pkv::RopeParams p{};
+    if (pair_axis) {
+        for (int i = 0; i < rot_dim / 2; ++i) {
+            if (pair_axis[i] >= num_axes) return PKV_ERR_INVALID_ARG;
+            p.axis_bits[i / 16] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i % 16));
+        }
+    }
+    if (num_tokens == 0) return PKV_OK;
+    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions || !cos_sin)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(cos_sin))
+        return PKV_ERR_INVALID_ARG;
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_out_stride = q_out_stride;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_cache = static_cast<__nv_bfloat16 *>(k_cache);
+    p.v_cache = static_cast<__nv_bfloat16 *>(v_cache);
+    p.slots = slot_mapping;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.max_positions = max_positions;
+    p.num_blocks = num_blocks;
+    p.err = err_word;
+    p.T = num_tokens;
+    p.Hq = num_heads;
+    p.Hkv = num_kv_heads;
+    p.rot = rot_dim;
+    p.axes = num_axes;
+    return cuda_status(pkv::launch_rope_kv_write(p, head_dim, interleaved != 0, sm_count(),
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_evict_tokens(void *k_cache, void *v_cache, const int32_t *block_tables,
+                            int max_blocks_per_seq, const int32_t *seq_lens,
+                            const int32_t *new_tables, int new_blocks_per_seq,
+                            const int32_t *keep_lens, const float *scores_in,
+                            int64_t scores_in_stride, float *scores_out, int64_t scores_out_stride,
+                            int32_t *kept, int sink, int recent, int num_seqs, int num_kv_heads,
+                            int head_dim, int64_t num_blocks, unsigned int *err_word, void *stream) {
+    if (num_seqs < 0 || num_seqs > 65535 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+        max_blocks_per_seq <= 0 || new_blocks_per_seq <= 0 || num_blocks <= 0 || sink < 0 ||
+        recent < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (num_blocks > INT32_MAX / PKV_BLOCK_TOKENS / num_kv_heads) return PKV_ERR_UNSUPPORTED;
+    const int64_t tokens = static_cast<int64_t>(max_blocks_per_seq) * PKV_BLOCK_TOKENS;
+    const int64_t new_tokens = static_cast<int64_t>(new_blocks_per_seq) * PKV_BLOCK_TOKENS;
+    if (tokens > INT32_MAX / 2 || new_tokens > INT32_MAX / 2) return PKV_ERR_INVALID_ARG;
+    if (scores_in_stride < tokens || scores_out_stride < new_tokens) return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_tables || !seq_lens || !new_tables || !keep_lens ||
+        !scores_in || !scores_out || !kept || scores_in == scores_out || block_tables == new_tables)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(scores_in) || !aligned4(scores_out) ||
+        !aligned4(kept))
+        return PKV_ERR_INVALID_ARG;
+    pkv::EvictParams p{};
+    p.k_cache = static_cast<__nv_bfloat16 *>(k_cache);
+    p.v_cache = static_cast<__nv_bfloat16 *>(v_cache);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.new_tables = new_tables;
+    p.keep_lens = keep_lens;
+    p.scores_in = scores_in;
+    p.scores_out = scores_out;
+    p.kept = kept;
+    p.in_stride = scores_in_stride;
+    p.out_stride = scores_out_stride;
+    p.num_blocks = num_blocks;
+    p.err = err_word;
+    p.W = max_blocks_per_seq;
+    p.NW = new_blocks_per_seq;
+    p.B = num_seqs;
+    p.Hkv = num_kv_heads;
+    p.sink = sink;
+    p.recent = recent;
+    return cuda_status(pkv::launch_evict(p, head_dim, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_paged_attention_decode(void *out, const void *q, const void *k_cache,

@@ -42,32 +42,6 @@ constexpr int kQWarp = kSoftmaxWarps + 2;  // + x: the Q rows of tile x
 constexpr int kThreads = (kSoftmaxWarps + 2 + kTiles) * 32;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-// ------------------------------------------------ packed f32x2 arithmetic
-// Two floats in one 64-bit register pair for the sm_100 f32x2 instructions.
-__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void f2unpack(uint64_t v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 template <int D>
 struct TcGeometry {
     static constexpr int kHalves = D / 64;
@@ -595,6 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O row, normalised, packed to bf16 and stored 64 columns at a
             // time; then O_x is handed back
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+            if (p.lse != nullptr && row_pos >= 0 && it.q0 >= 0 && it.q0 + r / G < p.num_tokens)
+                p.lse[(static_cast<size_t>(it.kvh) * p.num_tokens + it.q0) * G + r] = m_run + log2f(l_run);
             uint4 *dst = reinterpret_cast<uint4 *>(out_row);
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {

@@ -29,10 +29,12 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_OOM, ERR_CUDA = range(6)
 DEV_ERR_BAD_SLOT, DEV_ERR_BAD_BLOCK, DEV_ERR_BAD_LEN, DEV_ERR_TIMEOUT = 1, 2, 4, 8
+DEV_ERR_BAD_POS = 16
 DECODE_AUTO, DECODE_SINGLE, DECODE_SPLIT, DECODE_CLUSTER = 0, 1, 2, 4
 SWAP_OUT, SWAP_IN = 0, 1
 BLOCK_TOKENS = 16
 DEFAULT_PARTITION_TOKENS = 512
+ROPE_MAX_AXES = 4
 
 _P, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _sigs = {
@@ -85,6 +87,19 @@ _sigs = {
                                            _i64, _f32, _P, _P, _P, _i32, _i32, _i32, _P, _sz, _P,
                                            _P],
                                           _i32),
+    "pkv_rope_kv_write": ([_P, _P, _P, _P, _i64, _i64, _i64, _i64, _P, _P, _P, _P, _i32, _P, _P, _i64,
+                           _i32, _i32, _i32, _i32, _i32, _i32, _i64, _P, _P], _i32),
+    "pkv_decode_scored_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32], _sz),
+    "pkv_paged_attention_decode_scored": ([_P, _P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32,
+                                           _i32, _i64, _f32, _P, _P, _i64, _i32, _i32, _P, _sz, _P,
+                                           _P], _i32),
+    "pkv_prefill_scored_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
+    "pkv_paged_attention_prefill_scored": ([_P, _P, _i32, _P, _P, _P, _i32, _P, _P, _i32, _i32,
+                                            _i32, _i32, _i32, _i64, _f32, _P, _P, _i64, _i32, _P,
+                                            _sz, _P, _P], _i32),
+    "pkv_evict_tokens": ([_P, _P, _P, _i32, _P, _P, _i32, _P, _P, _i64, _P, _i64, _P, _i32, _i32,
+                          _i32, _i32, _i32, _i64, _P, _P], _i32),
+    "pkv_alloc_evict": ([_P, _P, _i32, _P], _i32),
     "pkv_alloc_seq_len": ([_P, _i64, _P], _i32),
     "pkv_alloc_slot_of": ([_P, _i64, _i64, _P], _i32),
 }
@@ -443,6 +458,228 @@ def suffix_blocks_bound(seq_lens, prefix_blocks) -> int:
     return int(max(1, (-(-lens // BLOCK_TOKENS) - pb).max()))
 
 
+# ------------------------------------------- rotary write, scores, eviction
+def _on_one_device(*tensors):
+    """The device all of the call's tensors are on."""
+    dev = tensors[0].device
+    if any(t is not None and t.device != dev for t in tensors):
+        raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _call(name, device, *args) -> None:
+    """Runs a library call on `device`'s current stream, with that device current."""
+    import torch
+
+    fn = getattr(_lib, name)
+    if device.index == torch.cuda.current_device():
+        code = fn(*args, _stream_ptr(device))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, _stream_ptr(device))
+    _check(code, name)
+
+
+def _scratch(device, workspace, nbytes):
+    """(pointer, bytes, tensor) of a call's workspace: the caller's, or one of the call's own
+    from torch's allocator (ordered with the stream; inside a graph capture the graph's own)."""
+    import torch
+
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    return _dev_tensor(workspace, torch.uint8, "workspace"), workspace.numel(), workspace
+
+
+def _token_rows(t, name, heads, d):
+    """Pointer and token stride of a [T, heads, d] bf16 tensor whose rows are contiguous."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, *,
+                  pair_axis=None, interleaved: bool = False, err=None) -> None:
+    """Rotary positions fused with the cache write (see include/pkv.h, pkv_rope_kv_write).
+    q, q_out [T, Hq, d], k, v [T, Hkv, d] bf16, each token's heads contiguous (slices of one
+    projection's output will do); positions [T] or [axes, T] int32; cos_sin [max_positions, rot]
+    float32 (rope_table makes one); pair_axis: the axis that turns each of the rot / 2 pairs
+    (a sequence of ints; with one axis it may be left out).  q_out may be q."""
+    import torch
+
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4 or cos_sin.dim() != 2 \
+            or positions.dim() not in (1, 2):
+        raise ValueError("shape mismatch")
+    T, hq, d = q.shape
+    hkv = k.shape[1]
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    rot = cos_sin.shape[1]
+    if q_out.shape != q.shape or k.shape != (T, hkv, d) or v.shape != k.shape \
+            or k_cache.shape != v_cache.shape or tuple(k_cache.shape[1:]) != (hkv, BLOCK_TOKENS, d) \
+            or slot_mapping.shape != (T,) or positions.shape[-1] != T:
+        raise ValueError("shape mismatch")
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != rot // 2:
+            raise ValueError("pair_axis: one axis for each of the rot / 2 pairs")
+    (qop, qos), (qp, qs), (kp, ks), (vp, vs) = (
+        _token_rows(x, n, h, d) for x, n, h in ((q_out, "q_out", hq), (q, "q", hq), (k, "k", hkv),
+                                                (v, "v", hkv)))
+    dev = _on_one_device(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, err)
+    _call("pkv_rope_kv_write", dev, qop, qp, kp, vp, qos, qs, ks, vs,
+          _dev_tensor(k_cache, torch.bfloat16, "k_cache"),
+          _dev_tensor(v_cache, torch.bfloat16, "v_cache"),
+          _dev_tensor(slot_mapping, torch.int64, "slot_mapping"),
+          _dev_tensor(positions, torch.int32, "positions"), axes, pair_axis,
+          _dev_tensor(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0], rot, int(interleaved),
+          T, hq, hkv, d, k_cache.shape[0],
+          _dev_tensor(err, torch.int32, "err") if err is not None else None)
+
+
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """The cos_sin table of rope_kv_write for frequencies base^(-2i / rot_dim), angles in float64."""
+    import torch
+
+    half = rot_dim // 2
+    freq = float(base) ** (-torch.arange(half, dtype=torch.float64) / half)
+    ang = torch.arange(max_positions, dtype=torch.float64)[:, None] * freq
+    return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous().to(device)
+
+
+def decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                  partition_tokens=DEFAULT_PARTITION_TOKENS) -> int:
+    return int(_lib.pkv_decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                      max_blocks_per_seq, partition_tokens))
+
+
+def _score_args(scores_in, scores_out, B, hkv, tokens):
+    import torch
+
+    if scores_out.dim() != 3 or tuple(scores_out.shape[:2]) != (B, hkv) or scores_out.shape[2] < tokens \
+            or (scores_in is not None and scores_in.shape != scores_out.shape):
+        raise ValueError("scores: [B, Hkv, at least the table's tokens], in and out alike")
+    return [_dev_tensor(scores_in, torch.float32, "scores_in") if scores_in is not None else None,
+            _dev_tensor(scores_out, torch.float32, "scores_out"), scores_out.shape[2]]
+
+
+def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_lens, scale, num_kv_heads,
+                                  scores_out, *, scores_in=None, k_new=None, v_new=None,
+                                  variant: int = DECODE_AUTO,
+                                  partition_tokens: int = DEFAULT_PARTITION_TOKENS,
+                                  workspace=None, err=None) -> None:
+    """paged_attention_decode (with k_new and v_new: paged_decode_step) that also adds each cached
+    token's attention weight to its score (see include/pkv.h, pkv_paged_attention_decode_scored).
+    scores_in, scores_out [B, Hkv, S] float32, S at least the table's tokens; scores_out may be
+    scores_in; without scores_in the step's weights alone."""
+    import torch
+
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new: both or neither")
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("shape mismatch")
+    B, hq, d = q.shape
+    W = block_tables.shape[1]
+    new_kv = () if k_new is None else (k_new, v_new)
+    if out.shape != q.shape or k_cache.shape != v_cache.shape \
+            or tuple(k_cache.shape[1:]) != (num_kv_heads, BLOCK_TOKENS, d) \
+            or block_tables.shape[0] != B or seq_lens.shape != (B,) \
+            or any(x.shape != (B, num_kv_heads, d) for x in new_kv):
+        raise ValueError("shape mismatch")
+    dev = _on_one_device(q, out, k_new, v_new, k_cache, v_cache, block_tables, seq_lens, scores_in,
+                         scores_out, workspace, err)
+    bf = torch.bfloat16
+    scores = _score_args(scores_in, scores_out, B, num_kv_heads, W * BLOCK_TOKENS)
+    need = decode_scored_workspace_bytes(B, hq, num_kv_heads, d, W, partition_tokens)
+    wp, wn, _keep = _scratch(dev, workspace, need)
+    _call("pkv_paged_attention_decode_scored", dev, _dev_tensor(out, bf, "out"), _dev_tensor(q, bf, "q"),
+          *([_dev_tensor(x, bf, n) for x, n in zip(new_kv, ("k_new", "v_new"))] or [None, None]),
+          _dev_tensor(k_cache, bf, "k_cache"), _dev_tensor(v_cache, bf, "v_cache"),
+          _dev_tensor(block_tables, torch.int32, "block_tables"), W,
+          _dev_tensor(seq_lens, torch.int32, "seq_lens"), B, hq, num_kv_heads, d, k_cache.shape[0],
+          float(scale), *scores, variant, partition_tokens, wp, wn,
+          _dev_tensor(err, torch.int32, "err") if err is not None else None)
+
+
+def prefill_scored_workspace_bytes(num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads,
+                                   max_blocks_per_seq, window=0) -> int:
+    return int(_lib.pkv_prefill_scored_workspace_bytes(num_tokens, num_seqs, max_query_len, num_heads,
+                                                       num_kv_heads, max_blocks_per_seq, window))
+
+
+def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, scale,
+                                   num_kv_heads, max_query_len: int, scores_out, *, scores_in=None,
+                                   window: int = 0, workspace=None, err=None) -> None:
+    """paged_attention_prefill that also adds the weights of each sequence's last `window` new tokens
+    (0: all of them) to the scores (see include/pkv.h, pkv_paged_attention_prefill_scored).
+    scores_in, scores_out [B, Hkv, S] float32, S at least the table's tokens; scores_out may be
+    scores_in."""
+    import torch
+
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("shape mismatch")
+    T, hq, d = q.shape
+    B, W = block_tables.shape
+    if out.shape != q.shape or k_cache.shape != v_cache.shape \
+            or tuple(k_cache.shape[1:]) != (num_kv_heads, BLOCK_TOKENS, d) \
+            or seq_lens.shape != (B,) or query_start.shape != (B + 1,):
+        raise ValueError("shape mismatch")
+    dev = _on_one_device(q, out, k_cache, v_cache, block_tables, seq_lens, query_start, scores_in,
+                         scores_out, workspace, err)
+    bf = torch.bfloat16
+    scores = _score_args(scores_in, scores_out, B, num_kv_heads, W * BLOCK_TOKENS)
+    args = (_dev_tensor(out, bf, "out"), _dev_tensor(q, bf, "q"), T,
+            _dev_tensor(k_cache, bf, "k_cache"), _dev_tensor(v_cache, bf, "v_cache"),
+            _dev_tensor(block_tables, torch.int32, "block_tables"), W,
+            _dev_tensor(seq_lens, torch.int32, "seq_lens"),
+            _dev_tensor(query_start, torch.int32, "query_start"), B, int(max_query_len), hq,
+            num_kv_heads, d, k_cache.shape[0], float(scale), *scores, int(window))
+    # the workspace's size goes by the device's SMs
+    with torch.cuda.device(dev):
+        need = prefill_scored_workspace_bytes(T, B, int(max_query_len), hq, num_kv_heads, W, int(window))
+    wp, wn, _keep = _scratch(dev, workspace, need)
+    _call("pkv_paged_attention_prefill_scored", dev, *args, wp, wn,
+          _dev_tensor(err, torch.int32, "err") if err is not None else None)
+
+
+def evict_tokens(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens, scores_in, scores_out,
+                 kept, *, sink: int = 0, recent: int = 0, err=None) -> None:
+    """Keep each sequence's keep_lens[b] tokens with the most weight -- each KV head its own, the
+    first `sink` and the last `recent` always -- and copy them together, in position order, into the
+    blocks of new_tables (see include/pkv.h, pkv_evict_tokens; BlockAllocator.evict gives such
+    tables).  block_tables [B, W], new_tables [B, NW], seq_lens, keep_lens [B] int32; scores_in
+    [B, Hkv, >= W * 16], scores_out [B, Hkv, >= NW * 16] float32; kept [B, Hkv, NW * 16] int32, the
+    kept tokens' old positions.  Entries past the kept tokens are not written."""
+    import torch
+
+    if k_cache.dim() != 4 or block_tables.dim() != 2 or new_tables.dim() != 2 or scores_in.dim() != 3 \
+            or scores_out.dim() != 3:
+        raise ValueError("shape mismatch")
+    nb, hkv, bt, d = k_cache.shape
+    (B, W), NW = block_tables.shape, new_tables.shape[1]
+    if v_cache.shape != k_cache.shape or bt != BLOCK_TOKENS or new_tables.shape[0] != B \
+            or seq_lens.shape != (B,) or keep_lens.shape != (B,) \
+            or tuple(scores_in.shape[:2]) != (B, hkv) or tuple(scores_out.shape[:2]) != (B, hkv) \
+            or kept.shape != (B, hkv, NW * BLOCK_TOKENS):
+        raise ValueError("shape mismatch")
+    dev = _on_one_device(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens, scores_in,
+                         scores_out, kept, err)
+    i32, f32 = torch.int32, torch.float32
+    _call("pkv_evict_tokens", dev, _dev_tensor(k_cache, torch.bfloat16, "k_cache"),
+          _dev_tensor(v_cache, torch.bfloat16, "v_cache"), _dev_tensor(block_tables, i32, "block_tables"),
+          W, _dev_tensor(seq_lens, i32, "seq_lens"), _dev_tensor(new_tables, i32, "new_tables"), NW,
+          _dev_tensor(keep_lens, i32, "keep_lens"), _dev_tensor(scores_in, f32, "scores_in"),
+          scores_in.shape[2], _dev_tensor(scores_out, f32, "scores_out"), scores_out.shape[2],
+          _dev_tensor(kept, i32, "kept"), int(sink), int(recent), B, hkv, d, nb,
+          _dev_tensor(err, i32, "err") if err is not None else None)
+
+
 # ---------------------------------------------------------------- allocator
 class AllocError(PkvError):
     @property
@@ -530,6 +767,15 @@ class BlockAllocator:
                                                   int(tables.shape[1]), _addr(tables), _addr(lens)),
                 "append_tokens_into")
         return out
+
+    def evict(self, seq_ids, keep_tokens) -> None:
+        """Shrink each sequence to keep_tokens[i] tokens in fresh blocks, all or none (for
+        evict_tokens: export() before and after gives its tables and lengths)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        keep = np.ascontiguousarray(keep_tokens, dtype=np.int64)
+        if ids.shape != keep.shape or ids.ndim != 1:
+            raise AllocError(ERR_INVALID_ARG, "evict: one keep_tokens entry for each sequence")
+        _acheck(_lib.pkv_alloc_evict(self._h, _addr(ids), len(ids), _addr(keep)), "evict")
 
     def free_seq(self, seq_id: int) -> None:
         _acheck(_lib.pkv_alloc_free_seq(self._h, int(seq_id)), "free_seq")

@@ -1,0 +1,214 @@
+"""The rotary write, the scored attention and the eviction on the host: argument
+checks that answer before any launch, workspace sizes, and the allocator's
+eviction against the reference model."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle.alloc_model import AllocError as ModelError, BlockManager
+from paged_kv_cache_459_b200 import build as pkv_build
+
+pkv_build.build()
+from paged_kv_cache_459_b200 import pkv  # noqa: E402
+
+FAKE = 0x10000  # 16-byte aligned, never dereferenced: validation rejects first
+INVALID, UNSUPPORTED, WORKSPACE = pkv.ERR_INVALID_ARG, pkv.ERR_UNSUPPORTED, pkv.ERR_WORKSPACE
+
+
+def rope(**kw):
+    a = dict(qo=FAKE, q=FAKE, k=FAKE, v=FAKE, sqo=512, sq=512, sk=256, sv=256, kc=FAKE, vc=FAKE, slots=FAKE,
+             pos=FAKE, axes=1, pair=None, table=FAKE, maxp=1024, rot=128, inter=0, T=4, Hq=4, Hkv=2, D=128, NB=8)
+    a.update(kw)
+    return pkv.lib().pkv_rope_kv_write(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED),
+    (dict(rot=8), INVALID), (dict(rot=136), INVALID), (dict(rot=0), INVALID), (dict(rot=72), INVALID),
+    (dict(axes=0), INVALID), (dict(axes=5, pair=bytes(64)), INVALID),
+    (dict(axes=2), INVALID),                               # several axes need to be told apart
+    (dict(axes=2, pair=bytes([2] * 64)), INVALID),         # an axis there is not
+    (dict(pair=bytes([1] * 64)), INVALID),
+    (dict(inter=2), INVALID), (dict(maxp=0), INVALID), (dict(NB=0), INVALID), (dict(T=-1), INVALID),
+    (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID),
+    (dict(sq=504), INVALID), (dict(sq=516), INVALID), (dict(sqo=8), INVALID), (dict(sk=128), INVALID),
+    (dict(sv=250), INVALID),
+    (dict(q=None), INVALID), (dict(table=None), INVALID), (dict(slots=None), INVALID), (dict(pos=None), INVALID),
+    (dict(q=FAKE + 8), INVALID), (dict(kc=FAKE + 2), INVALID), (dict(table=FAKE + 4), INVALID),
+    (dict(T=0, q=None, qo=None), pkv.OK),
+])
+def test_rope_argument_checks(kw, code):
+    assert rope(**kw) == code
+
+
+def decode(**kw):
+    a = dict(out=FAKE, q=FAKE, kn=None, vn=None, kc=FAKE, vc=FAKE, tables=FAKE, W=8, lens=FAKE, B=2, Hq=4, Hkv=2,
+             D=128, NB=64, scale=0.1, sin=None, sout=FAKE, stride=128, variant=0, part=512, ws=FAKE, wsb=1 << 30)
+    a.update(kw)
+    return pkv.lib().pkv_paged_attention_decode_scored(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(kn=FAKE), INVALID), (dict(vn=FAKE), INVALID), (dict(kn=FAKE + 2, vn=FAKE), INVALID),
+    (dict(sout=None), INVALID), (dict(sout=FAKE + 2), INVALID), (dict(sin=FAKE + 1), INVALID),
+    (dict(stride=127), INVALID), (dict(D=96), UNSUPPORTED), (dict(Hq=5), INVALID), (dict(variant=3), INVALID),
+    (dict(part=40), INVALID), (dict(ws=None), WORKSPACE), (dict(wsb=1024), WORKSPACE), (dict(ws=FAKE + 8), WORKSPACE),
+    (dict(scale=float("inf")), INVALID), (dict(B=0, out=None), pkv.OK),
+])
+def test_scored_decode_argument_checks(kw, code):
+    assert decode(**kw) == code
+
+
+def prefill(**kw):
+    a = dict(out=FAKE, q=FAKE, T=20, kc=FAKE, vc=FAKE, tables=FAKE, W=8, lens=FAKE, qs=FAKE, B=2, maxq=16, Hq=4,
+             Hkv=2, D=128, NB=64, scale=0.1, sin=None, sout=FAKE, stride=128, window=0, ws=FAKE, wsb=1 << 30)
+    a.update(kw)
+    return pkv.lib().pkv_paged_attention_prefill_scored(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), INVALID), (dict(maxq=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(D=32), UNSUPPORTED), (dict(Hq=258), UNSUPPORTED), (dict(Hq=5), INVALID), (dict(sout=None), INVALID),
+    (dict(stride=100), INVALID), (dict(qs=None), INVALID), (dict(q=None), INVALID), (dict(q=FAKE + 4), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(wsb=16), WORKSPACE), (dict(sin=FAKE + 2), INVALID),
+    (dict(W=1 << 20, stride=1 << 40), UNSUPPORTED), (dict(B=0), pkv.OK),
+])
+def test_scored_prefill_argument_checks(kw, code):
+    assert prefill(**kw) == code
+
+
+def evict(**kw):
+    a = dict(kc=FAKE, vc=FAKE, tables=FAKE, W=8, lens=FAKE, nt=FAKE + 256, NW=4, keep=FAKE, sin=FAKE, istr=128,
+             sout=FAKE + 512, ostr=64, kept=FAKE, sink=1, recent=2, B=2, Hkv=2, D=128, NB=64)
+    a.update(kw)
+    return pkv.lib().pkv_evict_tokens(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(sin=None), INVALID), (dict(kept=None), INVALID), (dict(sout=FAKE), INVALID), (dict(nt=FAKE), INVALID),
+    (dict(istr=127), INVALID), (dict(ostr=63), INVALID), (dict(sink=-1), INVALID), (dict(recent=-1), INVALID),
+    (dict(D=80), UNSUPPORTED), (dict(W=0), INVALID), (dict(NW=0), INVALID), (dict(B=70000), INVALID),
+    (dict(kc=FAKE + 8), INVALID), (dict(keep=None), INVALID), (dict(NB=1 << 28), UNSUPPORTED),
+    (dict(B=0, kc=None), pkv.OK),
+])
+def test_evict_argument_checks(kw, code):
+    assert evict(**kw) == code
+
+
+def test_scored_workspace_sizes():
+    up = lambda x: -(-x // 256) * 256  # noqa: E731
+    base = up(pkv.decode_workspace_bytes_for(pkv.DECODE_AUTO, 3, 28, 4, 128, 33))
+    assert pkv.decode_scored_workspace_bytes(3, 28, 4, 128, 33) == base + up(3 * 4 * 8 * 33 * 16 * 4) + up(3 * 28 * 4)
+    # one query head per KV head: one logit a token; groups above 8 in chunks
+    assert pkv.decode_scored_workspace_bytes(1, 2, 2, 64, 1) >= 2 * 16 * 4 + 8
+    assert pkv.decode_scored_workspace_bytes(2, 24, 2, 64, 5) >= 2 * 2 * 2 * 8 * 80 * 4
+    assert pkv.decode_scored_workspace_bytes(2, 5, 2, 64, 5) == 0
+    assert pkv.prefill_scored_workspace_bytes(-1, 2, 16, 4, 2, 8) == 0
+    assert pkv.prefill_scored_workspace_bytes(20, 2, 16, 4, 2, 8) >= 20 * 4 * 4
+
+
+def _same(a, m):
+    assert a.free_blocks() == m.free_blocks()
+    assert [a.refcount(b) for b in range(m.num_blocks)] == m.ref
+    ids = sorted(m.tables)
+    if ids:
+        w = max(1, max(len(m.tables[s]) for s in ids))
+        for x, y in zip(a.export(ids, w), m.export(ids, w)):
+            assert np.array_equal(x, y)
+
+
+def test_alloc_evict_takes_every_fresh_block_before_returning_one():
+    a = pkv.BlockAllocator(8)
+    a.add_seq(0, 33)
+    a.add_seq(1, 32)  # 3 + 2 blocks, 3 free
+    a.evict([0, 1], [17, 5])
+    tables, lens = a.export([0, 1], 2)
+    assert tables.tolist() == [[5, 6], [7, -1]] and lens.tolist() == [17, 5]
+    assert a.free_blocks() == [0, 1, 2, 3, 4]
+    with pytest.raises(pkv.AllocError) as e:
+        a.evict([0, 0], [1, 1])
+    assert e.value.kind == "invalid"
+    a.evict([1], [0])
+    assert a.export([1], 1)[0].tolist() == [[-1]] and a.free_blocks()[-1] == 7
+    a.evict([], [])
+
+
+def test_alloc_evict_leaves_shared_blocks_to_their_other_holders():
+    a = pkv.BlockAllocator(10)
+    a.add_seq(0, 40)
+    a.fork(0, 1)
+    a.evict([0], [20])
+    assert a.export([1], 3)[0].tolist() == [[0, 1, 2]] and a.export([0], 3)[0].tolist() == [[3, 4, -1]]
+    assert [a.refcount(b) for b in range(5)] == [1, 1, 1, 1, 1]
+
+
+def test_alloc_evict_against_the_model():
+    r = np.random.default_rng(5)
+    nb = 60
+    order = r.permutation(nb)
+    a, m = pkv.BlockAllocator(nb, order), BlockManager(nb, order)
+    done = {"evict": 0, "refused": 0}
+    for step in range(600):
+        ids = sorted(m.tables)
+        what = r.integers(0, 6)
+        if what == 0 or not ids:
+            args = ("add_seq", step, int(r.integers(0, 120)))
+        elif what == 1:
+            args = ("fork", int(r.choice(ids)), step)
+        elif what == 2:
+            args = ("append_token", int(r.choice(ids)))
+        elif what == 3:
+            args = ("free_seq", int(r.choice(ids)))
+        else:
+            some = [int(x) for x in r.choice(ids, size=int(r.integers(1, 4)))]
+            args = ("evict", some, [int(r.integers(0, m.lens[s] + 2)) for s in some])
+        got = []
+        for side in (a, m):
+            try:
+                getattr(side, args[0])(*args[1:])
+                got.append("ok")
+            except (pkv.AllocError, ModelError) as e:
+                got.append(e.kind)
+        assert got[0] == got[1], args
+        if args[0] == "evict":
+            done["evict" if got[0] == "ok" else "refused"] += 1
+        if args[0] == "append_token":
+            a.take_copies(), m.take_copies()
+        _same(a, m)
+    assert min(done.values()) > 20, done
+
+
+def test_binding_refuses_what_does_not_fit():
+    import torch
+
+    t = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    c = torch.zeros(4, 4, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    s = torch.zeros(2, 4, 16)
+    with pytest.raises(ValueError):   # host tensors
+        pkv.rope_kv_write(t, t, t, t, c, c, i.long(), i, torch.zeros(8, 64))
+    with pytest.raises(ValueError):   # shapes
+        pkv.rope_kv_write(t, t, t[:1], t, c, c, i.long(), i, torch.zeros(8, 64))
+    with pytest.raises(ValueError):   # one axis entry for each pair
+        pkv.rope_kv_write(t, t, t, t, c, c, i.long(), i, torch.zeros(8, 64), pair_axis=[0] * 31)
+    with pytest.raises(ValueError):
+        pkv.paged_attention_decode_scored(t, t, c, c, i.view(2, 1), i, 1.0, 4, s, k_new=t)
+    with pytest.raises(ValueError):   # a score row shorter than the table
+        pkv.paged_attention_decode_scored(t, t, c, c, torch.zeros(2, 2, dtype=torch.int32), i, 1.0, 4, s)
+    with pytest.raises(ValueError):
+        pkv.paged_attention_prefill_scored(t, t, c, c, i.view(2, 1), i, i, 1.0, 4, 1, s)
+    with pytest.raises(ValueError):   # kept: new table's tokens
+        pkv.evict_tokens(c, c, i.view(2, 1), i, i.view(2, 1), i, s, s, torch.zeros(2, 4, 8, dtype=torch.int32))
+
+
+def test_rope_table_is_the_cosines_and_sines_of_the_positions():
+    import torch
+
+    t = pkv.rope_table(70000, 64, 10000.0, device="cpu")
+    assert t.shape == (70000, 64) and t.dtype == torch.float32
+    p, i = 69999, 5
+    ang = p * 10000.0 ** (-2 * i / 64)
+    assert abs(float(t[p, i]) - np.cos(ang)) <= 2.0 ** -24 + 1e-11
+    assert abs(float(t[p, 32 + i]) - np.sin(ang)) <= 2.0 ** -24 + 1e-11
+    assert ctypes.sizeof(ctypes.c_float) == 4
