@@ -8,14 +8,15 @@
 // sequence's new table.  Keys carry their rotation already, so a token may
 // sit anywhere.  The old blocks are only read: they may be shared.
 //
-// evict_select_kernel: one CTA per (sequence, KV head) finds the
-// (m - r - s)-th largest score by a radix select over order-preserving
-// integer keys (11 + 11 + 10 bits, a histogram in shared memory each), then
-// one ordered pass writes the kept positions: every key above the threshold
-// and the first of those equal to it.  No sort, and the result does not depend
-// on the order of any atomic.
-// evict_copy_kernel: the rows; bound by HBM (each kept row read and written
-// once).
+// evict_select_kernel: a cluster of 1 to 4 CTAs per (sequence, KV head), each
+// CTA a slice of its tokens, finds the m-th largest of order-preserving integer
+// keys (the tokens that stay anyway hold the largest key) by a radix select:
+// 8 bits a pass, a histogram in each CTA's shared memory, the cluster's sum
+// read through distributed shared memory.  One ordered pass then writes the
+// kept positions: every key above the threshold and the first of those equal
+// to it.  No sort, and the result does not depend on the order of any atomic.
+// evict_copy_kernel: the rows and their scores; bound by HBM (each kept row
+// read and written once).
 #include <algorithm>
 
 #include "decode_common.cuh"
@@ -25,8 +26,6 @@ namespace pkv {
 namespace {
 
 using namespace dev;
-
-constexpr int kStagedTokens = 48 * 1024;  // keys kept in shared memory up to here (192 KB)
 
 // Larger key = higher score.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -58,8 +57,14 @@ __device__ __forceinline__ EvictRow evict_row(const EvictParams &p, int b, bool 
     return e;
 }
 
-// Block-wide exclusive scan of x over THREADS threads; *total gets the sum.
-template <int THREADS>
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kPer = 8;                     // consecutive tokens of a thread
+constexpr int kRound = kSelThreads * kPer;  // tokens a CTA holds in registers: 4096
+constexpr int kMaxSlices = 4;               // CTAs of a cluster
+constexpr int kCopies = 4;
+
+// Block-wide exclusive scan of x; *total gets the sum.
 __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = x;
@@ -73,7 +78,7 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
     __syncthreads();
     int before = 0, sum = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
+    for (int w = 0; w < kSelWarps; ++w) {
         const int v = warp_sums[w];
         before += w < warp ? v : 0;
         sum += v;
@@ -82,219 +87,284 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
     return before + incl - x;
 }
 
-constexpr int kBins = 2048;
-constexpr int kPerThread = 4;  // consecutive tokens a thread takes in the ordered pass
+// The keys of tokens [t0, t0 + kPer) of one row; the tokens that stay anyway
+// hold the largest key, which no score has.
+__device__ __forceinline__ void load_keys(const float *in, bool vec, int t0, const EvictRow &e, uint32_t (&k)[kPer]) {
+    float x[kPer];
+    if (vec && t0 + kPer <= e.len) {
+        *reinterpret_cast<float4 *>(x) = __ldg(reinterpret_cast<const float4 *>(in + t0));
+        *reinterpret_cast<float4 *>(x + 4) = __ldg(reinterpret_cast<const float4 *>(in + t0 + 4));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = t0 + i < e.len ? __ldg(in + t0 + i) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        k[i] = t0 + i < e.s || t0 + i >= e.len - e.r ? 0xFFFFFFFFu : score_key(x[i]);
+}
 
-template <int THREADS, bool STAGED>
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p) {
+// A few microseconds of barriers and first executions: 8 keys a thread stay in
+// registers (a round; longer slices read theirs again each pass).  For 256 rows
+// of about 2300 scores it takes 10 us, with 16 keys unrolled 17, with the keys
+// in shared memory 14; for 64 rows of 32768, four CTAs a row take 22 us, two
+// 32 and eight 27 (their five cluster barriers), one with all keys in shared
+// memory 38.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, int slices) {
     pdl_launch_dependents();
-    extern __shared__ uint32_t keys[];  // [len] when STAGED
-    __shared__ int hist[kBins];
-    __shared__ int warp_sums[THREADS / 32];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    // A pass counts into kCopies histograms, a lane into its own (scores share few
+    // leading bytes, and a warp's updates of one word go one after another), ...
+    __shared__ __align__(16) int spread[256 * kCopies];
+    __shared__ int hist[4][256];  // ... summed here; one per pass: another CTA may still read the last pass's
+    __shared__ int warp_sums[kSelWarps];
+    __shared__ int found[2];      // the pass's bin, the keys above it
+    __shared__ int counts[2];     // this slice's keys above and at the threshold
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const auto clear = [&] {
+        for (int i = tid; i < 256 * kCopies / 4; i += kSelThreads) reinterpret_cast<int4 *>(spread)[i] = make_int4(0, 0, 0, 0);
+    };
+    clear();
     pdl_wait_primary();
     bool bad;
     const EvictRow e = evict_row(p, b, &bad);
-    if (bad && h == 0 && tid == 0) flag(p.err, PKV_DEV_ERR_BAD_LEN);
+    if (bad && h == 0 && rank == 0 && tid == 0) flag(p.err, PKV_DEV_ERR_BAD_LEN);
     const size_t row = static_cast<size_t>(b) * p.Hkv + h;
     const float *in = p.scores_in + row * p.in_stride;
-    float *out = p.scores_out + row * p.out_stride;
     int32_t *kept = p.kept + row * (static_cast<size_t>(p.NW) * kBlockTokens);
-    if (e.m == e.len) {  // nothing goes
-        for (int t = tid; t < e.len; t += THREADS) {
-            kept[t] = t;
-            out[t] = in[t];
-        }
+    // this CTA's tokens [lo, hi), lo a multiple of kPer (whole cluster: the same e)
+    const int per = ((e.len + slices - 1) / slices + kPer - 1) / kPer * kPer;
+    const int lo = min(rank * per, e.len), hi = min(lo + per, e.len);
+    if (e.m == e.len || e.m == 0) {  // nothing goes, or everything
+        if (e.m > 0)
+            for (int t = lo + tid; t < hi; t += kSelThreads) kept[t] = t;
         return;
     }
-    const int lo = e.s, hi = e.len - e.r;  // the tokens that compete
-    const int want = e.m - e.r - e.s;      // 0 <= want < hi - lo
-    if (STAGED) {
-        for (int t = lo + tid; t < hi; t += THREADS) keys[t] = score_key(__ldg(in + t));
-    }
-    const auto key_at = [&](int t) { return STAGED ? keys[t] : score_key(__ldg(in + t)); };
-    // the want-th largest key: `prefix` its bits so far, `need` its rank among
-    // the keys that share them
-    uint32_t prefix = 0;
-    int need = want;
-    if (want > 0) {
-        if (tid == 0) {
-            s_prefix = 0;
-            s_need = want;
-        }
+    const bool vec = (reinterpret_cast<uintptr_t>(in) & 15u) == 0;
+    const int rounds = (per + kRound - 1) / kRound;
+    uint32_t k0[kPer];
+    load_keys(in, vec, lo + tid * kPer, e, k0);
+    __syncthreads();  // cleared
+    uint32_t prefix = 0;  // the m-th largest key's bits so far
+    int need = e.m;       // its rank among the keys that share them
+    bool all = false;     // every key that shares them is kept
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const int bits = pass == 2 ? 10 : 11;
-            const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + bits);
-            for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
-            __syncthreads();  // also: keys staged, s_prefix and s_need written
-            prefix = s_prefix;
-            need = s_need;
-            for (int t = lo + tid; t < hi; t += THREADS) {
-                const uint32_t k = key_at(t);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
-            }
-            __syncthreads();
-            // bins from the top: thread i owns the kBins / THREADS bins below those of thread i - 1
-            constexpr int kOwn = kBins / THREADS;
-            int own[kOwn], sum = 0;
+    for (int pass = 0; pass < 4 && !all; ++pass) {
+        const int shift = 24 - 8 * pass;
+        const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+#pragma unroll 1
+        for (int r = 0; r < rounds; ++r) {
+            const int t0 = lo + r * kRound + tid * kPer;
+            uint32_t k[kPer];
+            if (r == 0) {
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                own[i] = hist[kBins - 1 - (tid * kOwn + i)];
-                sum += own[i];
+                for (int i = 0; i < kPer; ++i) k[i] = k0[i];
+            } else {
+                load_keys(in, vec, t0, e, k);
             }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (t0 + i < hi && (k[i] & mask) == prefix)
+                    atomicAdd(&spread[((k[i] >> shift) & 255) * kCopies + lane % kCopies], 1);
+        }
+        __syncthreads();
+        int mine = 0;  // thread i < 256: this slice's, then the cluster's count of bin 255 - i
+        if (tid < 256) {
+#pragma unroll
+            for (int i = 0; i < kCopies; i += 4) {
+                const int4 v = *reinterpret_cast<const int4 *>(spread + (255 - tid) * kCopies + i);
+                mine += (v.x + v.y) + (v.z + v.w);
+            }
+            hist[pass][255 - tid] = mine;
+        }
+        if (slices > 1) {
+            cluster_arrive_release();
+            cluster_wait_acquire();
+            if (tid < 256) {
+                const uint32_t at = smem_u32(&hist[pass][255 - tid]);
+                mine = 0;
+#pragma unroll
+                for (int c = 0; c < kMaxSlices; ++c)
+                    if (c < slices) mine += static_cast<int>(ld_dsmem_u32(dsmem_addr(at, c)));
+            }
+        }
+        // the keys in the bins above
+        int incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+        }
+        if (lane == 31) warp_sums[warp] = incl;
+        __syncthreads();  // and: this pass's copies are read
+        clear();
+        if (tid < 256) {
+            int above = incl - mine;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) above += w < warp ? warp_sums[w] : 0;
+            if (above < need && need <= above + mine) {  // exactly one thread
+                found[0] = (255 - tid) | (need == above + mine ? 256 : 0);
+                found[1] = above;
+            }
+        }
+        __syncthreads();
+        prefix |= static_cast<uint32_t>(found[0] & 255) << shift;
+        need -= found[1];
+        // every key of the bin is kept: the remaining bits need no telling apart
+        all = (found[0] & 256) && prefix != 0;
+    }
+    // kept: keys above the threshold, and the first `need` equal to it
+    const uint32_t threshold = all ? prefix - 1 : prefix;
+    if (all) need = 0;
+    // this slice's first place: the keys above and at the threshold in the slices before it
+    int above0 = 0, equal0 = 0;
+    const auto count = [&](const uint32_t (&k)[kPer], int t0) {
+        int n = 0;  // keys above the threshold, and (from bit 16) equal to it: at most kRound of each
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (t0 + i < hi) n += k[i] > threshold ? 1 : k[i] == threshold ? 1 << 16 : 0;
+        return n;
+    };
+    int total0, packed0 = block_scan(count(k0, lo + tid * kPer), warp_sums, &total0);
+    if (slices > 1) {
+        int above = total0 & 0xFFFF, equal = total0 >> 16;
+#pragma unroll 1
+        for (int r = 1; r < rounds; ++r) {
+            const int t0 = lo + r * kRound + tid * kPer;
+            uint32_t k[kPer];
+            load_keys(in, vec, t0, e, k);
             int total;
-            int above = block_scan<THREADS>(sum, warp_sums, &total);
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                if (above < need && need <= above + own[i]) {  // exactly one bin of one thread
-                    s_prefix = prefix | (static_cast<uint32_t>(kBins - 1 - (tid * kOwn + i)) << shift);
-                    s_need = need - above;
-                }
-                above += own[i];
-            }
+            block_scan(count(k, t0), warp_sums, &total);
+            above += total & 0xFFFF;
+            equal += total >> 16;
         }
-        __syncthreads();
-        prefix = s_prefix;
-        need = s_need;
-    } else {
-        __syncthreads();
-    }
-    // In position order: sinks, keys above the threshold and the first `need`
-    // equal to it, recent tokens.  A token's place = the kept ones before it.
-    for (int t = tid; t < e.s; t += THREADS) {
-        kept[t] = t;
-        out[t] = in[t];
-    }
-    for (int t = hi + tid; t < e.len; t += THREADS) {
-        const int i = e.m - (e.len - t);
-        kept[i] = t;
-        out[i] = in[t];
-    }
-    if (want == 0) return;
-    int above_before = 0, equal_before = 0;
-    for (int base = lo; base < hi; base += THREADS * kPerThread) {
-        const int t0 = base + tid * kPerThread;
-        uint32_t k[kPerThread];
-        int n_above = 0, n_equal = 0;
+        if (tid == 0) {
+            counts[0] = above;
+            counts[1] = equal;
+        }
+        cluster_arrive_release();
+        cluster_wait_acquire();
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            k[i] = t0 + i < hi ? key_at(t0 + i) : 0u;
+        for (int c = 0; c < kMaxSlices - 1; ++c)
+            if (c < rank) {
+                above0 += static_cast<int>(ld_dsmem_u32(dsmem_addr(smem_u32(&counts[0]), c)));
+                equal0 += static_cast<int>(ld_dsmem_u32(dsmem_addr(smem_u32(&counts[1]), c)));
+            }
+        cluster_arrive_release();  // this CTA reads no other's memory from here on
+    }
+    // a kept token's place: those kept before it
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r) {
+        const int t0 = lo + r * kRound + tid * kPer;
+        uint32_t k[kPer];
+        int total = total0, packed = packed0;
+        if (r == 0) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) k[i] = k0[i];
+        } else {
+            load_keys(in, vec, t0, e, k);
+            packed = block_scan(count(k, t0), warp_sums, &total);
+        }
+        int a = above0 + (packed & 0xFFFF), q = equal0 + (packed >> 16);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
             if (t0 + i < hi) {
-                n_above += k[i] > prefix;
-                n_equal += k[i] == prefix;
-            }
-        }
-        // both counts in one scan: at most THREADS * kPerThread <= 4096 of each
-        int total;
-        const int packed = block_scan<THREADS>(n_above | (n_equal << 16), warp_sums, &total);
-        int a = above_before + (packed & 0xFFFF), q = equal_before + (packed >> 16);
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int t = t0 + i;
-            if (t < hi) {
-                const bool gt = k[i] > prefix, eq = k[i] == prefix;
-                if (gt || (eq && q < need)) {
-                    const int at = e.s + a + min(q, need);
-                    kept[at] = t;
-                    out[at] = in[t];
-                }
+                const bool gt = k[i] > threshold, eq = k[i] == threshold;
+                if (gt || (eq && q < need)) kept[a + min(q, need)] = t0 + i;
                 a += gt;
                 q += eq;
             }
         }
-        above_before += total & 0xFFFF;
-        equal_before += total >> 16;
+        above0 += total & 0xFFFF;
+        equal0 += total >> 16;
     }
+    if (slices > 1) cluster_wait_acquire();  // the others have read this CTA's counts
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kWarpTokens = 32;  // kept tokens of one warp
-constexpr int kCopyTokens = kCopyThreads / 32 * kWarpTokens;
+constexpr int kGroup = 32;  // kept tokens of a warp, one lane each for their addresses
 
-// A warp moves one row of K (its first D / 8 lanes) and V (the next) at a
-// time per 32 / (D / 4) tokens, 8 rows' loads in flight.
+// A warp moves 32 kept tokens; a pass of it one row of K and one of V (D = 128:
+// half a warp each) or two of both, kBatch passes' loads in flight.  Many warps
+// with few rows each, not few with many: the addresses are three loads that
+// wait for one another (length, kept position, table entry), and warps in
+// their copy hide those of the next.
 template <int D>
-__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const EvictParams p) {
     pdl_launch_dependents();
     constexpr int kVec = D / 8;             // 16-byte vectors of a row
-    constexpr int kRows = 32 / (2 * kVec);  // tokens of one pass (K and V)
+    constexpr int kRows = 32 / (2 * kVec);  // tokens of one pass
     constexpr int kBatch = 8;
-    static_assert(kWarpTokens == 32 && 32 % (kBatch * kRows) == 0, "one lane per token of the warp");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    static_assert(kGroup == 32 && kGroup % (kBatch * kRows) == 0, "one lane per token");
+    const int lane = threadIdx.x & 31;
     const int h = blockIdx.y, b = blockIdx.z;
+    const int first = (blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5)) * kGroup;
     pdl_wait_primary();
     bool bad;
     const EvictRow e = evict_row(p, b, &bad);
-    const int first = blockIdx.x * kCopyTokens + warp * kWarpTokens;
     if (first >= e.m) return;
-    const int n = min(kWarpTokens, e.m - first);
-    // lane i: source and destination row of token first + i (-1: left out)
-    long long src = -1, dst = -1;
-    if (lane < n) {
-        const int i = first + lane;
-        const int t = __ldcg(p.kept + (static_cast<size_t>(b) * p.Hkv + h) * (static_cast<size_t>(p.NW) * kBlockTokens) + i);
-        const int32_t from = __ldg(p.block_tables + static_cast<size_t>(b) * p.W + t / kBlockTokens);
+    const int i = first + lane;
+    int src = -1, dst = -1;  // rows of the caches (num_blocks * Hkv * 16 < 2^31), -1: none
+    if (i < e.m) {
+        const size_t row = static_cast<size_t>(b) * p.Hkv + h;
+        const int t = __ldcg(p.kept + row * (static_cast<size_t>(p.NW) * kBlockTokens) + i);
         const int32_t to = __ldg(p.new_tables + static_cast<size_t>(b) * p.NW + i / kBlockTokens);
+        const int32_t from = __ldg(p.block_tables + static_cast<size_t>(b) * p.W + t / kBlockTokens);
+        p.scores_out[row * p.out_stride + i] = __ldg(p.scores_in + row * p.in_stride + t);
         if (from >= 0 && from < p.num_blocks && to >= 0 && to < p.num_blocks) {
-            src = (static_cast<long long>(from) * p.Hkv + h) * kBlockTokens + t % kBlockTokens;
-            dst = (static_cast<long long>(to) * p.Hkv + h) * kBlockTokens + i % kBlockTokens;
+            src = (from * p.Hkv + h) * kBlockTokens + t % kBlockTokens;
+            dst = (to * p.Hkv + h) * kBlockTokens + i % kBlockTokens;
         } else {
             flag(p.err, PKV_DEV_ERR_BAD_BLOCK);
         }
     }
     const int sub = lane / (2 * kVec);  // which token of a pass
-    const int vec = lane % kVec;
     const bool is_v = (lane / kVec) & 1;
-    uint4 *cache = reinterpret_cast<uint4 *>(is_v ? p.v_cache : p.k_cache);
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += kBatch * kRows) {
+    uint4 *cache = reinterpret_cast<uint4 *>(is_v ? p.v_cache : p.k_cache) + lane % kVec;
+#pragma unroll
+    for (int i0 = 0; i0 < kGroup; i0 += kBatch * kRows) {
         uint4 x[kBatch];
-        long long to[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kRows + sub;
-            // (lanes at or past n hold -1)
-            const long long from = __shfl_sync(0xffffffffu, src, i);
-            to[j] = __shfl_sync(0xffffffffu, dst, i);
-            if (from >= 0) x[j] = __ldcs(cache + from * kVec + vec);
+            const int from = __shfl_sync(0xffffffffu, src, i0 + j * kRows + sub);
+            if (from >= 0) x[j] = __ldcs(cache + static_cast<long long>(from) * kVec);
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (to[j] >= 0) cache[to[j] * kVec + vec] = x[j];
+        for (int j = 0; j < kBatch; ++j) {
+            const int to = __shfl_sync(0xffffffffu, dst, i0 + j * kRows + sub);
+            if (to >= 0) cache[static_cast<long long>(to) * kVec] = x[j];
+        }
     }
-}
-
-template <int THREADS, bool STAGED>
-cudaError_t launch_select(const EvictParams &p, size_t smem, cudaStream_t stream) {
-    auto kern = evict_select_kernel<THREADS, STAGED>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_dependent_smem(kern, dim3(static_cast<unsigned>(p.Hkv), static_cast<unsigned>(p.B)), dim3(THREADS),
-                                 smem, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int head_dim, cudaStream_t stream) {
+    // a CTA for each kRound tokens of the longest row, at most kMaxSlices
     const long long tokens = static_cast<long long>(p.W) * kBlockTokens;
-    cudaError_t e;
-    if (tokens <= 8192)
-        e = launch_select<256, true>(p, static_cast<size_t>(tokens) * 4, stream);
-    else if (tokens <= kStagedTokens)
-        e = launch_select<1024, true>(p, static_cast<size_t>(tokens) * 4, stream);
-    else
-        e = launch_select<1024, false>(p, 0, stream);
+    int slices = 1;
+    while (slices < kMaxSlices && static_cast<long long>(slices) * kRound < tokens) slices *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(slices), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(p.B));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(slices);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = slices > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, slices);
     if (e != cudaSuccess) return e;
     const long long most = static_cast<long long>(p.NW) * kBlockTokens;
-    const dim3 grid(static_cast<unsigned>((most + kCopyTokens - 1) / kCopyTokens), static_cast<unsigned>(p.Hkv),
+    constexpr int kTokens = kCopyThreads / 32 * kGroup;  // of a CTA
+    const dim3 grid(static_cast<unsigned>((most + kTokens - 1) / kTokens), static_cast<unsigned>(p.Hkv),
                     static_cast<unsigned>(p.B));
-    if (head_dim == 128) return launch_dependent(evict_copy_kernel<128>, grid, dim3(kCopyThreads), stream, p);
-    if (head_dim == 64) return launch_dependent(evict_copy_kernel<64>, grid, dim3(kCopyThreads), stream, p);
-    return cudaErrorInvalidValue;
+    return launch_dependent(head_dim == 128 ? evict_copy_kernel<128> : evict_copy_kernel<64>, grid, dim3(kCopyThreads),
+                            stream, p);
 }
 
 }  // namespace pkv

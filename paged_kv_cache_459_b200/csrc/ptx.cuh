@@ -116,6 +116,12 @@ __device__ __forceinline__ void st_dsmem_f32(uint32_t remote, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t remote) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+    return v;
+}
+
 // Orders this thread's earlier memory accesses (and, after a CTA barrier,
 // its CTA's) before its later ones at cluster scope.
 __device__ __forceinline__ void fence_acq_rel_cluster() {

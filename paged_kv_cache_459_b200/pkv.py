@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from functools import lru_cache
 
 import numpy as np
 
@@ -156,6 +157,32 @@ def _stream_ptr(device) -> int:
     import torch
 
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _ptr(t, dtype, name, dev: int) -> int:
+    """_dev_tensor for the calls whose tensors must all be on device `dev`: four tensor
+    methods a tensor, since a small call's time is its argument marshalling."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev_tensor(t, dtype, name)  # says what is wrong
+    raise ValueError(f"{name}: tensors must be on one device")
+
+
+def _run(fn, name, dev: int, *args) -> None:
+    """fn(*args, stream) on device `dev`'s current stream, with that device current."""
+    import torch
+
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream)
+    if code != OK:
+        raise PkvError(code, name)
 
 
 def paged_kv_write(k, v, k_cache, v_cache, slot_mapping, err=None) -> None:
@@ -459,50 +486,41 @@ def suffix_blocks_bound(seq_lens, prefix_blocks) -> int:
 
 
 # ------------------------------------------- rotary write, scores, eviction
-def _on_one_device(*tensors):
-    """The device all of the call's tensors are on."""
-    dev = tensors[0].device
-    if any(t is not None and t.device != dev for t in tensors):
-        raise ValueError("tensors must be on one device")
+def _cuda_index(t, name) -> int:
+    """The index of the CUDA device a tensor is on."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
     return dev
 
 
-def _call(name, device, *args) -> None:
-    """Runs a library call on `device`'s current stream, with that device current."""
-    import torch
-
-    fn = getattr(_lib, name)
-    if device.index == torch.cuda.current_device():
-        code = fn(*args, _stream_ptr(device))
-    else:
-        with torch.cuda.device(device):
-            code = fn(*args, _stream_ptr(device))
-    _check(code, name)
-
-
-def _scratch(device, workspace, nbytes):
+def _scratch(dev, workspace, nbytes):
     """(pointer, bytes, tensor) of a call's workspace: the caller's, or one of the call's own
     from torch's allocator (ordered with the stream; inside a graph capture the graph's own)."""
     import torch
 
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    return _dev_tensor(workspace, torch.uint8, "workspace"), workspace.numel(), workspace
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), nbytes, workspace
+    return _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel(), workspace
 
 
-def _token_rows(t, name, heads, d):
+def _token_rows(t, name, heads, d, dev):
     """Pointer and token stride of a [T, heads, d] bf16 tensor whose rows are contiguous."""
     import torch
 
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != torch.bfloat16:
+    if _cuda_index(t, name) != dev:
+        raise ValueError(f"{name}: tensors must be on one device")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    st, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != d):
         raise ValueError(f"{name}: each token's heads must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+    return t.data_ptr(), st
 
 
 def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, *,
@@ -514,33 +532,38 @@ def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos
     (a sequence of ints; with one axis it may be left out).  q_out may be q."""
     import torch
 
-    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4 or cos_sin.dim() != 2 \
-            or positions.dim() not in (1, 2):
-        raise ValueError("shape mismatch")
-    T, hq, d = q.shape
-    hkv = k.shape[1]
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    rot = cos_sin.shape[1]
-    if q_out.shape != q.shape or k.shape != (T, hkv, d) or v.shape != k.shape \
-            or k_cache.shape != v_cache.shape or tuple(k_cache.shape[1:]) != (hkv, BLOCK_TOKENS, d) \
-            or slot_mapping.shape != (T,) or positions.shape[-1] != T:
+    try:
+        T, hq, d = q.shape
+        _, hkv, _ = k.shape
+        nb, *tile = k_cache.shape
+        max_positions, rot = cos_sin.shape
+        *axes, n = positions.shape
+        axes, = axes or (1,)
+    except ValueError:
+        raise ValueError("shape mismatch") from None
+    if q_out.shape != q.shape or k.shape != (T, hkv, d) or v.shape != k.shape or n != T \
+            or tile != [hkv, BLOCK_TOKENS, d] or v_cache.shape != k_cache.shape \
+            or slot_mapping.shape != (T,):
         raise ValueError("shape mismatch")
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != rot // 2:
             raise ValueError("pair_axis: one axis for each of the rot / 2 pairs")
-    (qop, qos), (qp, qs), (kp, ks), (vp, vs) = (
-        _token_rows(x, n, h, d) for x, n, h in ((q_out, "q_out", hq), (q, "q", hq), (k, "k", hkv),
-                                                (v, "v", hkv)))
-    dev = _on_one_device(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, err)
-    _call("pkv_rope_kv_write", dev, qop, qp, kp, vp, qos, qs, ks, vs,
-          _dev_tensor(k_cache, torch.bfloat16, "k_cache"),
-          _dev_tensor(v_cache, torch.bfloat16, "v_cache"),
-          _dev_tensor(slot_mapping, torch.int64, "slot_mapping"),
-          _dev_tensor(positions, torch.int32, "positions"), axes, pair_axis,
-          _dev_tensor(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0], rot, int(interleaved),
-          T, hq, hkv, d, k_cache.shape[0],
-          _dev_tensor(err, torch.int32, "err") if err is not None else None)
+    dev = _cuda_index(q, "q")
+    qop, qos = _token_rows(q_out, "q_out", hq, d, dev)
+    qp, qs = _token_rows(q, "q", hq, d, dev)
+    kp, ks = _token_rows(k, "k", hkv, d, dev)
+    vp, vs = _token_rows(v, "v", hkv, d, dev)
+    if T == 1:  # a single row's stride says nothing
+        qos = qs = hq * d
+        ks = vs = hkv * d
+    bf = torch.bfloat16
+    _run(_lib.pkv_rope_kv_write, "pkv_rope_kv_write", dev, qop, qp, kp, vp, qos, qs, ks, vs,
+         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
+         _ptr(slot_mapping, torch.int64, "slot_mapping", dev),
+         _ptr(positions, torch.int32, "positions", dev), axes, pair_axis,
+         _ptr(cos_sin, torch.float32, "cos_sin", dev), max_positions, rot, interleaved, T, hq, hkv, d,
+         nb, None if err is None else _ptr(err, torch.int32, "err", dev))
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -553,20 +576,23 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
     return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous().to(device)
 
 
+@lru_cache(maxsize=256)
 def decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
                                   partition_tokens=DEFAULT_PARTITION_TOKENS) -> int:
     return int(_lib.pkv_decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
                                                       max_blocks_per_seq, partition_tokens))
 
 
-def _score_args(scores_in, scores_out, B, hkv, tokens):
+def _score_args(scores_in, scores_out, B, hkv, tokens, dev):
     import torch
 
-    if scores_out.dim() != 3 or tuple(scores_out.shape[:2]) != (B, hkv) or scores_out.shape[2] < tokens \
+    b, h, stride = scores_out.shape if scores_out.dim() == 3 else (-1, -1, -1)
+    if b != B or h != hkv or stride < tokens \
             or (scores_in is not None and scores_in.shape != scores_out.shape):
         raise ValueError("scores: [B, Hkv, at least the table's tokens], in and out alike")
-    return [_dev_tensor(scores_in, torch.float32, "scores_in") if scores_in is not None else None,
-            _dev_tensor(scores_out, torch.float32, "scores_out"), scores_out.shape[2]]
+    f32 = torch.float32
+    return (None if scores_in is None else _ptr(scores_in, f32, "scores_in", dev),
+            _ptr(scores_out, f32, "scores_out", dev), stride)
 
 
 def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_lens, scale, num_kv_heads,
@@ -582,35 +608,54 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
 
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new: both or neither")
-    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+    try:
+        B, hq, d = q.shape
+        rows, W = block_tables.shape
+        nb, *tile = k_cache.shape
+    except ValueError:
+        raise ValueError("shape mismatch") from None
+    hkv = num_kv_heads
+    if out.shape != q.shape or tile != [hkv, BLOCK_TOKENS, d] or v_cache.shape != k_cache.shape \
+            or rows != B or seq_lens.shape != (B,) \
+            or (k_new is not None and (k_new.shape != (B, hkv, d) or v_new.shape != (B, hkv, d))):
         raise ValueError("shape mismatch")
-    B, hq, d = q.shape
-    W = block_tables.shape[1]
-    new_kv = () if k_new is None else (k_new, v_new)
-    if out.shape != q.shape or k_cache.shape != v_cache.shape \
-            or tuple(k_cache.shape[1:]) != (num_kv_heads, BLOCK_TOKENS, d) \
-            or block_tables.shape[0] != B or seq_lens.shape != (B,) \
-            or any(x.shape != (B, num_kv_heads, d) for x in new_kv):
-        raise ValueError("shape mismatch")
-    dev = _on_one_device(q, out, k_new, v_new, k_cache, v_cache, block_tables, seq_lens, scores_in,
-                         scores_out, workspace, err)
-    bf = torch.bfloat16
-    scores = _score_args(scores_in, scores_out, B, num_kv_heads, W * BLOCK_TOKENS)
-    need = decode_scored_workspace_bytes(B, hq, num_kv_heads, d, W, partition_tokens)
-    wp, wn, _keep = _scratch(dev, workspace, need)
-    _call("pkv_paged_attention_decode_scored", dev, _dev_tensor(out, bf, "out"), _dev_tensor(q, bf, "q"),
-          *([_dev_tensor(x, bf, n) for x, n in zip(new_kv, ("k_new", "v_new"))] or [None, None]),
-          _dev_tensor(k_cache, bf, "k_cache"), _dev_tensor(v_cache, bf, "v_cache"),
-          _dev_tensor(block_tables, torch.int32, "block_tables"), W,
-          _dev_tensor(seq_lens, torch.int32, "seq_lens"), B, hq, num_kv_heads, d, k_cache.shape[0],
-          float(scale), *scores, variant, partition_tokens, wp, wn,
-          _dev_tensor(err, torch.int32, "err") if err is not None else None)
+    dev = _cuda_index(q, "q")
+    bf, i32 = torch.bfloat16, torch.int32
+    sin, sout, stride = _score_args(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS, dev)
+    wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else
+                             decode_scored_workspace_bytes(B, hq, hkv, d, W, partition_tokens))
+    _run(_lib.pkv_paged_attention_decode_scored, "pkv_paged_attention_decode_scored", dev,
+         _ptr(out, bf, "out", dev), _ptr(q, bf, "q", dev),
+         None if k_new is None else _ptr(k_new, bf, "k_new", dev),
+         None if v_new is None else _ptr(v_new, bf, "v_new", dev),
+         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
+         _ptr(block_tables, i32, "block_tables", dev), W, _ptr(seq_lens, i32, "seq_lens", dev), B, hq,
+         hkv, d, nb, scale, sin, sout, stride, variant, partition_tokens, wp, wn,
+         None if err is None else _ptr(err, i32, "err", dev))
+
+
+@lru_cache(maxsize=256)
+def _prefill_scored_bytes(dev, *sizes) -> int:
+    import torch
+
+    if dev < 0:
+        return int(_lib.pkv_prefill_scored_workspace_bytes(*sizes))
+    with torch.cuda.device(dev):  # the size goes by the device's SMs
+        return int(_lib.pkv_prefill_scored_workspace_bytes(*sizes))
 
 
 def prefill_scored_workspace_bytes(num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads,
-                                   max_blocks_per_seq, window=0) -> int:
-    return int(_lib.pkv_prefill_scored_workspace_bytes(num_tokens, num_seqs, max_query_len, num_heads,
-                                                       num_kv_heads, max_blocks_per_seq, window))
+                                   max_blocks_per_seq, window=0, device=None) -> int:
+    """Workspace of paged_attention_prefill_scored for these sizes on a CUDA device (default: the
+    current one)."""
+    import torch
+
+    if device is not None:
+        dev = torch.device(device).index
+    else:
+        dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _prefill_scored_bytes(-1 if dev is None else dev, num_tokens, num_seqs, max_query_len,
+                                 num_heads, num_kv_heads, max_blocks_per_seq, window)
 
 
 def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, scale,
@@ -622,30 +667,27 @@ def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_l
     scores_in."""
     import torch
 
-    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
-        raise ValueError("shape mismatch")
-    T, hq, d = q.shape
-    B, W = block_tables.shape
-    if out.shape != q.shape or k_cache.shape != v_cache.shape \
-            or tuple(k_cache.shape[1:]) != (num_kv_heads, BLOCK_TOKENS, d) \
+    try:
+        T, hq, d = q.shape
+        B, W = block_tables.shape
+        nb, *tile = k_cache.shape
+    except ValueError:
+        raise ValueError("shape mismatch") from None
+    hkv = num_kv_heads
+    if out.shape != q.shape or tile != [hkv, BLOCK_TOKENS, d] or v_cache.shape != k_cache.shape \
             or seq_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise ValueError("shape mismatch")
-    dev = _on_one_device(q, out, k_cache, v_cache, block_tables, seq_lens, query_start, scores_in,
-                         scores_out, workspace, err)
-    bf = torch.bfloat16
-    scores = _score_args(scores_in, scores_out, B, num_kv_heads, W * BLOCK_TOKENS)
-    args = (_dev_tensor(out, bf, "out"), _dev_tensor(q, bf, "q"), T,
-            _dev_tensor(k_cache, bf, "k_cache"), _dev_tensor(v_cache, bf, "v_cache"),
-            _dev_tensor(block_tables, torch.int32, "block_tables"), W,
-            _dev_tensor(seq_lens, torch.int32, "seq_lens"),
-            _dev_tensor(query_start, torch.int32, "query_start"), B, int(max_query_len), hq,
-            num_kv_heads, d, k_cache.shape[0], float(scale), *scores, int(window))
-    # the workspace's size goes by the device's SMs
-    with torch.cuda.device(dev):
-        need = prefill_scored_workspace_bytes(T, B, int(max_query_len), hq, num_kv_heads, W, int(window))
-    wp, wn, _keep = _scratch(dev, workspace, need)
-    _call("pkv_paged_attention_prefill_scored", dev, *args, wp, wn,
-          _dev_tensor(err, torch.int32, "err") if err is not None else None)
+    dev = _cuda_index(q, "q")
+    bf, i32 = torch.bfloat16, torch.int32
+    sin, sout, stride = _score_args(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS, dev)
+    wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else _prefill_scored_bytes(
+        dev, T, B, max_query_len, hq, hkv, W, window))
+    _run(_lib.pkv_paged_attention_prefill_scored, "pkv_paged_attention_prefill_scored", dev,
+         _ptr(out, bf, "out", dev), _ptr(q, bf, "q", dev), T,
+         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
+         _ptr(block_tables, i32, "block_tables", dev), W, _ptr(seq_lens, i32, "seq_lens", dev),
+         _ptr(query_start, i32, "query_start", dev), B, max_query_len, hq, hkv, d, nb, scale, sin, sout,
+         stride, window, wp, wn, None if err is None else _ptr(err, i32, "err", dev))
 
 
 def evict_tokens(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens, scores_in, scores_out,
@@ -658,26 +700,27 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens
     kept tokens' old positions.  Entries past the kept tokens are not written."""
     import torch
 
-    if k_cache.dim() != 4 or block_tables.dim() != 2 or new_tables.dim() != 2 or scores_in.dim() != 3 \
-            or scores_out.dim() != 3:
-        raise ValueError("shape mismatch")
-    nb, hkv, bt, d = k_cache.shape
-    (B, W), NW = block_tables.shape, new_tables.shape[1]
-    if v_cache.shape != k_cache.shape or bt != BLOCK_TOKENS or new_tables.shape[0] != B \
-            or seq_lens.shape != (B,) or keep_lens.shape != (B,) \
-            or tuple(scores_in.shape[:2]) != (B, hkv) or tuple(scores_out.shape[:2]) != (B, hkv) \
+    try:
+        nb, hkv, bt, d = k_cache.shape
+        B, W = block_tables.shape
+        rows, NW = new_tables.shape
+        ib, ih, istride = scores_in.shape
+        ob, oh, ostride = scores_out.shape
+    except ValueError:
+        raise ValueError("shape mismatch") from None
+    if v_cache.shape != k_cache.shape or bt != BLOCK_TOKENS or rows != B or ib != B or ob != B \
+            or ih != hkv or oh != hkv or seq_lens.shape != (B,) or keep_lens.shape != (B,) \
             or kept.shape != (B, hkv, NW * BLOCK_TOKENS):
         raise ValueError("shape mismatch")
-    dev = _on_one_device(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens, scores_in,
-                         scores_out, kept, err)
-    i32, f32 = torch.int32, torch.float32
-    _call("pkv_evict_tokens", dev, _dev_tensor(k_cache, torch.bfloat16, "k_cache"),
-          _dev_tensor(v_cache, torch.bfloat16, "v_cache"), _dev_tensor(block_tables, i32, "block_tables"),
-          W, _dev_tensor(seq_lens, i32, "seq_lens"), _dev_tensor(new_tables, i32, "new_tables"), NW,
-          _dev_tensor(keep_lens, i32, "keep_lens"), _dev_tensor(scores_in, f32, "scores_in"),
-          scores_in.shape[2], _dev_tensor(scores_out, f32, "scores_out"), scores_out.shape[2],
-          _dev_tensor(kept, i32, "kept"), int(sink), int(recent), B, hkv, d, nb,
-          _dev_tensor(err, i32, "err") if err is not None else None)
+    dev = _cuda_index(k_cache, "k_cache")
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    _run(_lib.pkv_evict_tokens, "pkv_evict_tokens", dev,
+         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
+         _ptr(block_tables, i32, "block_tables", dev), W, _ptr(seq_lens, i32, "seq_lens", dev),
+         _ptr(new_tables, i32, "new_tables", dev), NW, _ptr(keep_lens, i32, "keep_lens", dev),
+         _ptr(scores_in, f32, "scores_in", dev), istride, _ptr(scores_out, f32, "scores_out", dev),
+         ostride, _ptr(kept, i32, "kept", dev), sink, recent, B, hkv, d, nb,
+         None if err is None else _ptr(err, i32, "err", dev))
 
 
 # ---------------------------------------------------------------- allocator

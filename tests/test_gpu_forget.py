@@ -433,10 +433,10 @@ def test_evict(lens, keep, hkv, d, sink, recent):
     evict_case(lens, keep, hkv, d, sink, recent, seed=sum(lens))
 
 
-@pytest.mark.parametrize("width", [512, 513, 3000, 3200])
+@pytest.mark.parametrize("width", [256, 257, 513, 1025, 3000])
 def test_evict_table_widths(width):
-    """The select's forms: 256 threads up to 8192 tokens, 1024 above, keys in shared memory up to 49152."""
-    evict_case([width * BT - 5, 8000], [2000, 4000], 2, 64, 4, 64, seed=width, width=width)
+    """One CTA a row, clusters of two and four, and slices of several rounds."""
+    evict_case([width * BT - 5, 4000], [2000, 3000], 2, 64, 4, 64, seed=width, width=width)
 
 
 def test_evict_equal_scores_keep_the_lowest_positions():
