@@ -9,7 +9,10 @@
 // s = scale * log2(e) * q.k (fp32, 4 bytes a query head beside the 4 d bytes
 // of a KV head's K and V) in a workspace and the row's log-sum-exp; the
 // kernel below turns them into 2^(s - lse), sums over the KV head's query
-// heads in a fixed order and adds.
+// heads in a fixed order and adds.  The workspace is read back while most of
+// it is in L2 (K and V are loaded evict-first).  (Adding inside the unit when
+// it is done, to save the launch, took the single pass from 223 to 235 us at
+// 256 sequences: 128 threads a CTA wait for L2 where they could stream K and V.)
 #include "decode_unit.cuh"
 
 namespace pkv {
@@ -24,48 +27,82 @@ __global__ void __launch_bounds__(128)
                                const __grid_constant__ CUtensorMap tmv, const DecodeParams p) {
     if (p.order != nullptr) {
         pdl_wait_primary();
-        decode_unit<D, 4, 2, MMA, MODE, true>(tmk, tmv, p, blockIdx.x, blockIdx.y,
-                                              __ldg(p.order + blockIdx.z));
+        decode_unit<D, 4, 2, MMA, MODE, true>(tmk, tmv, p, blockIdx.x, blockIdx.y, __ldg(p.order + blockIdx.z));
     } else {
-        decode_unit<D, 4, 2, MMA, MODE, true>(tmk, tmv, p, blockIdx.x, blockIdx.y,
-                                              static_cast<int>(blockIdx.z), true);
+        decode_unit<D, 4, 2, MMA, MODE, true>(tmk, tmv, p, blockIdx.x, blockIdx.y, static_cast<int>(blockIdx.z), true);
     }
 }
 
-// One thread per (sequence, KV head, token).
+// A thread's tokens of one (sequence, KV head): t0, t0 + kAddThreads, ...  Every
+// load is issued before any is used; the logits of a block that was not read are
+// loaded too (the workspace holds a place for every table entry) and left out.
 constexpr int kAddThreads = 256;
+constexpr int kAddTokens = 2;
 
-__global__ void __launch_bounds__(kAddThreads)
-    score_add_kernel(const DecodeParams p, const ScoreParams sp) {
+template <int V>  // logits of a load: 4 where the width is a multiple of it, else 1
+__global__ void __launch_bounds__(kAddThreads) score_add_kernel(const DecodeParams p, const ScoreParams sp) {
     pdl_launch_dependents();
     const int g = blockIdx.y, b = blockIdx.z;
-    const int t = blockIdx.x * kAddThreads + threadIdx.x;
-    pdl_wait_primary();
+    const int t0 = blockIdx.x * (kAddThreads * kAddTokens) + threadIdx.x;
     int len = __ldg(p.seq_lens + b);
     len = len < 0 ? 0 : min(len, p.W * kBlockTokens);
-    if (t >= len) return;
-    const size_t tokens = static_cast<size_t>(p.W) * kBlockTokens;
-    const int32_t phys = __ldg(p.block_tables + static_cast<size_t>(b) * p.W + t / kBlockTokens);
-    float w = 0.f;
-    if (phys >= 0 && phys < p.num_blocks) {  // a block that was not read has no weight
-        for (int c = 0; c < p.chunks; ++c) {
-            const float *s = p.logits +
-                             (((static_cast<size_t>(b) * p.Hkv + g) * p.chunks + c) * tokens + t) * p.logit_width;
-            const float *lse = p.lse + static_cast<size_t>(b) * p.Hq + g * p.group + 8 * c;
-            const int heads = min(8, p.group - 8 * c);
+    bool live[kAddTokens];
+    int32_t phys[kAddTokens];
 #pragma unroll
-            for (int h = 0; h < 8; ++h)
-                if (h < heads) w += ex2_approx(s[h] - lse[h]);
+    for (int i = 0; i < kAddTokens; ++i) {
+        const int t = t0 + i * kAddThreads;
+        live[i] = t < len;
+        phys[i] = live[i] ? __ldg(p.block_tables + static_cast<size_t>(b) * p.W + t / kBlockTokens) : -1;
+    }
+    pdl_wait_primary();  // the lengths and tables are host-written; the rest is the grids' before
+    if (blockIdx.x * (kAddThreads * kAddTokens) >= static_cast<unsigned>(len)) return;
+    const size_t row = (static_cast<size_t>(b) * p.Hkv + g);
+    const size_t at = row * sp.stride + t0;
+    float before[kAddTokens], w[kAddTokens];
+#pragma unroll
+    for (int i = 0; i < kAddTokens; ++i) {
+        before[i] = sp.scores_in != nullptr && t0 + i * kAddThreads < len - 1 ? sp.scores_in[at + i * kAddThreads] : 0.f;
+        w[i] = 0.f;
+    }
+    const size_t tokens = static_cast<size_t>(p.W) * kBlockTokens;
+    for (int c = 0; c < p.chunks; ++c) {
+        const int heads = min(8, p.group - 8 * c);
+        const float *lse = p.lse + static_cast<size_t>(b) * p.Hq + g * p.group + 8 * c;
+        const float *s = p.logits + ((row * p.chunks + c) * tokens + t0) * p.logit_width;
+#pragma unroll
+        for (int h = 0; h < 8; h += V) {
+            if (h >= heads) break;
+            float x[kAddTokens][V];
+#pragma unroll
+            for (int i = 0; i < kAddTokens; ++i) {
+                const float *src = s + static_cast<size_t>(i) * kAddThreads * p.logit_width + h;
+                if constexpr (V == 4) {
+                    const float4 v = live[i] ? __ldcg(reinterpret_cast<const float4 *>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[i][0] = v.x;
+                    x[i][1] = v.y;
+                    x[i][2] = v.z;
+                    x[i][3] = v.w;
+                } else {
+                    x[i][0] = live[i] ? __ldcg(src) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (h + e >= heads) break;
+                const float l = __ldg(lse + h + e);
+#pragma unroll
+                for (int i = 0; i < kAddTokens; ++i) w[i] += ex2_approx(x[i][e] - l);
+            }
         }
     }
-    const size_t at = (static_cast<size_t>(b) * p.Hkv + g) * sp.stride + t;
-    const float before = sp.scores_in != nullptr && t < len - 1 ? sp.scores_in[at] : 0.f;
-    sp.scores_out[at] = before + w;
+#pragma unroll
+    for (int i = 0; i < kAddTokens; ++i)
+        if (live[i])
+            sp.scores_out[at + i * kAddThreads] = before[i] + (phys[i] >= 0 && phys[i] < p.num_blocks ? w[i] : 0.f);
 }
 
 template <int D, bool MMA, int MODE>
-cudaError_t launch_one(const CUtensorMap &tmk, const CUtensorMap &tmv, const DecodeParams &p,
-                       cudaStream_t stream) {
+cudaError_t launch_one(const CUtensorMap &tmk, const CUtensorMap &tmv, const DecodeParams &p, cudaStream_t stream) {
     using G = Geometry<D, 4, 2>;
     constexpr int kSmem = G::kSmemBytes + (MODE == kModeCluster ? cluster_land_bytes<D, MMA>() : 0);
     auto kern = paged_decode_scored_kernel<D, MMA, MODE>;
@@ -115,9 +152,11 @@ cudaError_t launch_decode_scored(const CUtensorMap &tmk, const CUtensorMap &tmv,
         e = p.group > 1 ? launch_m<64, true>(tmk, tmv, p, mode, stream)
                         : launch_m<64, false>(tmk, tmv, p, mode, stream);
     if (e != cudaSuccess) return e;
-    const unsigned gx = static_cast<unsigned>((static_cast<long long>(p.W) * kBlockTokens + kAddThreads - 1) / kAddThreads);
-    return launch_dependent(score_add_kernel, dim3(gx, static_cast<unsigned>(p.Hkv), static_cast<unsigned>(p.B)),
-                            dim3(kAddThreads), stream, p, sp);
+    constexpr int kTokens = kAddThreads * kAddTokens;
+    const unsigned gx = static_cast<unsigned>((static_cast<long long>(p.W) * kBlockTokens + kTokens - 1) / kTokens);
+    return launch_dependent(p.logit_width % 4 == 0 ? score_add_kernel<4> : score_add_kernel<1>,
+                            dim3(gx, static_cast<unsigned>(p.Hkv), static_cast<unsigned>(p.B)), dim3(kAddThreads),
+                            stream, p, sp);
 }
 
 }  // namespace pkv

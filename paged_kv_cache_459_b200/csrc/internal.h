@@ -149,9 +149,10 @@ struct PrefillScoreParams {
     int window;         // new tokens counted (INT_MAX: all)
     int max_query_len;
     int tile_tokens;    // tokens of a 128-row query tile (128 / group)
+    int units;          // work units (set by the launcher)
 };
 cudaError_t launch_prefill_scores(const CUtensorMap &tmk, const CUtensorMap &tmq,
-                                  const PrefillScoreParams &p, int head_dim, cudaStream_t stream);
+                                  const PrefillScoreParams &p, int head_dim, int num_sms, cudaStream_t stream);
 // The splits launch_prefill_scores cuts these sizes into (its workspace depends on it).
 int prefill_score_splits(int B, int Hkv, int group, int W, int window, int max_query_len, int num_sms);
 

@@ -765,7 +765,8 @@ pkv_status pkv_paged_attention_prefill_scored(
         return PKV_ERR_INVALID_ARG;
     if (num_blocks > INT32_MAX / PKV_BLOCK_TOKENS / num_kv_heads) return PKV_ERR_UNSUPPORTED;
     const int64_t row_tokens = static_cast<int64_t>(max_blocks_per_seq) * PKV_BLOCK_TOKENS;
-    if (row_tokens > 65535 * 128) return PKV_ERR_UNSUPPORTED;  // key tiles of a launch
+    if (row_tokens > INT32_MAX / 2) return PKV_ERR_INVALID_ARG;
+    if (row_tokens / 128 > INT32_MAX / 128 / num_seqs / num_kv_heads) return PKV_ERR_UNSUPPORTED;  // work units
     if (score_stride < row_tokens) return PKV_ERR_INVALID_ARG;
     const int counted = window_or_all(window);
     const PrefillScoreWorkspace sw = prefill_score_workspace(
@@ -774,7 +775,7 @@ pkv_status pkv_paged_attention_prefill_scored(
         return PKV_ERR_WORKSPACE;
 
     const int64_t rows = num_blocks * num_kv_heads * PKV_BLOCK_TOKENS;
-    CUtensorMap tmk, tmv, tmk_scores, tmq;
+    CUtensorMap tmk, tmv, tmq;
     pkv::PrefillScoreParams p{};
     p.pp.out = static_cast<__nv_bfloat16 *>(out);
     p.pp.q = static_cast<const __nv_bfloat16 *>(q);
@@ -800,7 +801,6 @@ pkv_status pkv_paged_attention_prefill_scored(
     if (!encode_cache_map(&tmk, k_cache, rows, head_dim) ||
         !encode_cache_map(&tmv, v_cache, rows, head_dim))
         return PKV_ERR_CUDA;
-    tmk_scores = tmk;
     // without new tokens there is no q: no unit loads a query tile
     tmq = tmk;
     if (num_tokens > 0 && !encode_q_map(&tmq, q, num_tokens, num_heads, head_dim, group, p.tile_tokens))
@@ -811,7 +811,7 @@ pkv_status pkv_paged_attention_prefill_scored(
             pkv::launch_prefill_tc(tmk, tmv, p.pp, head_dim, p.max_query_len, sm_count(), s);
         if (e != cudaSuccess) return cuda_status(e);
     }
-    return cuda_status(pkv::launch_prefill_scores(tmk_scores, tmq, p, head_dim, s));
+    return cuda_status(pkv::launch_prefill_scores(tmk, tmq, p, head_dim, sm_count(), s));
 }
 
 pkv_status pkv_rope_kv_write(void *q_out, const void *q, const void *k, const void *v,

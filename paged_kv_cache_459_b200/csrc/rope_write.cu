@@ -20,7 +20,7 @@ namespace {
 using namespace dev;
 
 constexpr int kRopeThreads = 128;
-constexpr int kBatch = 4;  // rows a lane has in flight
+constexpr int kBatch = 3;  // rows a lane has in flight
 
 // 8 pairs: a holds the first elements, b the second (half-split), or the 16
 // elements in order (interleaved).
@@ -73,6 +73,24 @@ __global__ void __launch_bounds__(kRopeThreads)
         ea = item * 8;
         eb = ea + half;
     }
+
+    uint4 a[kBatch], b[kBatch];
+    const auto load = [&](int base) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int r = base + j * kRows + lane / kItems;
+            if (r < row1) {
+                const __nv_bfloat16 *src =
+                    r < p.Hq ? p.q + t * p.q_stride + r * D
+                    : r < p.Hq + p.Hkv ? p.k + t * p.k_stride + (r - p.Hq) * D
+                                       : p.v + t * p.v_stride + (r - p.Hq - p.Hkv) * D;
+                a[j] = *reinterpret_cast<const uint4 *>(src + ea);
+                b[j] = *reinterpret_cast<const uint4 *>(src + eb);
+            }
+        }
+    };
+    // the first rows are on their way while slot, position and then the table's row are read
+    load(row0);
 
     const long long slot = __ldg(p.slots + t);
     long long pos[8];
@@ -128,19 +146,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     }
 
     for (int base = row0; base < row1; base += kRows * kBatch) {
-        uint4 a[kBatch], b[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int r = base + j * kRows + lane / kItems;
-            if (r < row1) {
-                const __nv_bfloat16 *src =
-                    r < p.Hq ? p.q + t * p.q_stride + r * D
-                    : r < p.Hq + p.Hkv ? p.k + t * p.k_stride + (r - p.Hq) * D
-                                       : p.v + t * p.v_stride + (r - p.Hq - p.Hkv) * D;
-                a[j] = *reinterpret_cast<const uint4 *>(src + ea);
-                b[j] = *reinterpret_cast<const uint4 *>(src + eb);
-            }
-        }
+        if (base > row0) load(base);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int r = base + j * kRows + lane / kItems;

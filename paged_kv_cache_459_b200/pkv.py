@@ -513,14 +513,14 @@ def _token_rows(t, name, heads, d, dev):
     """Pointer and token stride of a [T, heads, d] bf16 tensor whose rows are contiguous."""
     import torch
 
-    if _cuda_index(t, name) != dev:
-        raise ValueError(f"{name}: tensors must be on one device")
+    st, sh, sd = t.stride()
+    if t.dtype is torch.bfloat16 and t.get_device() == dev and sd == 1 and (sh == d or heads == 1):
+        return t.data_ptr(), st
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    st, sh, sd = t.stride()
-    if sd != 1 or (heads > 1 and sh != d):
-        raise ValueError(f"{name}: each token's heads must be contiguous")
-    return t.data_ptr(), st
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors must be on one device")
+    raise ValueError(f"{name}: each token's heads must be contiguous")
 
 
 def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, *,

@@ -72,7 +72,7 @@ def prefill(**kw):
     (dict(D=32), UNSUPPORTED), (dict(Hq=258), UNSUPPORTED), (dict(Hq=5), INVALID), (dict(sout=None), INVALID),
     (dict(stride=100), INVALID), (dict(qs=None), INVALID), (dict(q=None), INVALID), (dict(q=FAKE + 4), INVALID),
     (dict(ws=None), WORKSPACE), (dict(wsb=16), WORKSPACE), (dict(sin=FAKE + 2), INVALID),
-    (dict(W=1 << 20, stride=1 << 40), UNSUPPORTED), (dict(B=0), pkv.OK),
+    (dict(W=1 << 25, stride=1 << 40), UNSUPPORTED), (dict(W=1 << 26, stride=1 << 40), INVALID), (dict(B=0), pkv.OK),
 ])
 def test_scored_prefill_argument_checks(kw, code):
     assert prefill(**kw) == code
