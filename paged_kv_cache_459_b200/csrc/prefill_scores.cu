@@ -44,7 +44,7 @@ struct ScoreGeometry {
     static constexpr int kQ = kTileBytes;                   // + stage * kTileBytes
     static constexpr int kNeg = kQ + kQStages * kTileBytes;  // -lse of a tile's rows, beside each S buffer
     static constexpr int kBars = kNeg + kSBuffers * kCols * 4;
-    static constexpr int kNumBars = 2 + 2 * kQStages + 3 * kSBuffers;
+    static constexpr int kNumBars = 2 + 2 * kQStages + 2 * kSBuffers;
     static constexpr int kTmemSlot = kBars + kNumBars * 8;    // then the abort flag, a flag for each S buffer
     static constexpr int kSmemBytes = kTmemSlot + 8 + 4 * kSBuffers + 1024;
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -191,7 +191,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const auto s_full = [&](int x) { return bar0 + 8 * (2 + 2 * kQStages + x); };
     const auto s_empty = [&](int x) { return bar0 + 8 * (2 + 2 * kQStages + kSBuffers + x); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Geo::kTmemSlot);
-    const auto n_full = [&](int x) { return bar0 + 8 * (2 + 2 * kQStages + 2 * kSBuffers + x); };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Geo::kTmemSlot + 4);
     volatile int *odd_flag = abort_flag + 1;  // [kSBuffers]: a row of the tile has a sum that is not finite
 
@@ -203,9 +202,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(q_empty(s), 1);
         }
         for (int x = 0; x < kSBuffers; ++x) {
-            mbar_init(s_full(x), 1);
+            mbar_init(s_full(x), 2);  // its products and its rows' -lse
             mbar_init(s_empty(x), kExpWarps);
-            mbar_init(n_full(x), 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -364,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 odd = __any_sync(0xffffffffu, odd);
                 if (lane == 0) odd_flag[x] = odd;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(n_full(x));
+                if (lane == 0) mbar_arrive(s_full(x));
                 if (i + 1 < u.n)
                     odd = load(u, i + 1, x4);
                 else if (kn >= 0)
@@ -392,11 +390,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             float total = 0.f;
             for (int i = 0; i < u.n; ++i, ++g) {
                 const int x = g % kSBuffers;
-                const uint32_t parity = static_cast<uint32_t>((g / kSBuffers) & 1);
-                ok = mbar_wait(n_full(x), parity, kWaitLimitNs) && mbar_wait(s_full(x), parity, kWaitLimitNs) && !*abort_flag;
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full(x), static_cast<uint32_t>((g / kSBuffers) & 1), kWaitLimitNs));
                 if (!ok) break;
                 tc::fence_after();
+                uint32_t sr[2][32];
+                const uint32_t ts = t_s + kCols * x;
+                tc::ld32(ts, sr[0]);
                 // columns [c_lo, c_hi) are rows at or after this thread's key
                 const int tok = u.tok + i * p.tile_tokens;
                 const int c_hi = min(p.tile_tokens, u.sq.nq - tok) * G;
@@ -409,9 +408,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // infinities and NaN as they are.
                 const bool odd = odd_flag[x];
                 uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-                uint32_t sr[2][32];
-                const uint32_t ts = t_s + kCols * x;
-                tc::ld32(ts, sr[0]);
                 const auto chunk = [&](const uint32_t *r, int c0) {
                     // no row of the chunk sees a key of the warp / every one sees every key
                     if (diagonal && __all_sync(0xffffffffu, c_lo >= c0 + 32)) return;
@@ -509,9 +505,9 @@ int prefill_score_splits(int B, int Hkv, int group, int W, int window, int max_q
     const long long units = static_cast<long long>(B) * Hkv * ((static_cast<long long>(W) * kBlockTokens + kKeys - 1) / kKeys);
     const long long tile_tokens = std::max(1, kCols / group);
     const long long tiles = (std::min(window, max_query_len) + tile_tokens - 1) / tile_tokens;
-    // two waves of two CTAs per SM, at least two tiles each
+    // two waves of two CTAs per SM, a tile each at least (short prompts: 20 us a call, 22 with two tiles, 25 with eight)
     const long long want = (4LL * num_sms + units - 1) / std::max(1LL, units);
-    return static_cast<int>(std::max(1LL, std::min({want, tiles / 2, 64LL})));
+    return static_cast<int>(std::max(1LL, std::min({want, tiles, 64LL})));
 }
 
 cudaError_t launch_prefill_scores(const CUtensorMap &tmk, const CUtensorMap &tmq, const PrefillScoreParams &p,

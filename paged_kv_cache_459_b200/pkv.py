@@ -162,11 +162,8 @@ def _stream_ptr(device) -> int:
 def _ptr(t, dtype, name, dev: int) -> int:
     """_dev_tensor for the calls whose tensors must all be on device `dev`: four tensor
     methods a tensor, since a small call's time is its argument marshalling."""
-    try:
-        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     _dev_tensor(t, dtype, name)  # says what is wrong
     raise ValueError(f"{name}: tensors must be on one device")
 
@@ -486,16 +483,12 @@ def suffix_blocks_bound(seq_lens, prefix_blocks) -> int:
 
 
 # ------------------------------------------- rotary write, scores, eviction
-def _cuda_index(t, name) -> int:
-    """The index of the CUDA device a tensor is on."""
-    import torch
-
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be on a CUDA device")
-    return dev
+def _not_one_device(*named):
+    """Raises what is wrong with tensors of which some are not on the first one's CUDA device."""
+    for t, name in named:
+        if t is not None and t.device.type != "cuda":
+            raise ValueError(f"{name} must be on a CUDA device")
+    raise ValueError("tensors must be on one device")
 
 
 def _scratch(dev, workspace, nbytes):
@@ -518,8 +511,8 @@ def _token_rows(t, name, heads, d, dev):
         return t.data_ptr(), st
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: tensors must be on one device")
+    if t.get_device() != dev or dev < 0:
+        _not_one_device((t, name))
     raise ValueError(f"{name}: each token's heads must be contiguous")
 
 
@@ -535,21 +528,24 @@ def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos
     try:
         T, hq, d = q.shape
         _, hkv, _ = k.shape
-        nb, *tile = k_cache.shape
+        nb = k_cache.shape[0]
         max_positions, rot = cos_sin.shape
-        *axes, n = positions.shape
-        axes, = axes or (1,)
     except ValueError:
         raise ValueError("shape mismatch") from None
-    if q_out.shape != q.shape or k.shape != (T, hkv, d) or v.shape != k.shape or n != T \
-            or tile != [hkv, BLOCK_TOKENS, d] or v_cache.shape != k_cache.shape \
-            or slot_mapping.shape != (T,):
+    axes = positions.shape[0] if positions.ndim == 2 else 1
+    cache = (nb, hkv, BLOCK_TOKENS, d)
+    kv = (T, hkv, d)
+    if q_out.shape != (T, hq, d) or k.shape != kv or v.shape != kv or k_cache.shape != cache \
+            or v_cache.shape != cache or slot_mapping.shape != (T,) \
+            or positions.shape != ((T,) if positions.ndim == 1 else (axes, T)):
         raise ValueError("shape mismatch")
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != rot // 2:
             raise ValueError("pair_axis: one axis for each of the rot / 2 pairs")
-    dev = _cuda_index(q, "q")
+    dev = q.get_device()
+    if dev < 0:
+        _not_one_device((q, "q"))
     qop, qos = _token_rows(q_out, "q_out", hq, d, dev)
     qp, qs = _token_rows(q, "q", hq, d, dev)
     kp, ks = _token_rows(k, "k", hkv, d, dev)
@@ -586,9 +582,9 @@ def decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, m
 def _score_args(scores_in, scores_out, B, hkv, tokens, dev):
     import torch
 
-    b, h, stride = scores_out.shape if scores_out.dim() == 3 else (-1, -1, -1)
-    if b != B or h != hkv or stride < tokens \
-            or (scores_in is not None and scores_in.shape != scores_out.shape):
+    stride = scores_out.shape[-1]
+    rows = (B, hkv, stride)
+    if scores_out.shape != rows or stride < tokens or (scores_in is not None and scores_in.shape != rows):
         raise ValueError("scores: [B, Hkv, at least the table's tokens], in and out alike")
     f32 = torch.float32
     return (None if scores_in is None else _ptr(scores_in, f32, "scores_in", dev),
@@ -611,15 +607,18 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
     try:
         B, hq, d = q.shape
         rows, W = block_tables.shape
-        nb, *tile = k_cache.shape
+        nb = k_cache.shape[0]
     except ValueError:
         raise ValueError("shape mismatch") from None
     hkv = num_kv_heads
-    if out.shape != q.shape or tile != [hkv, BLOCK_TOKENS, d] or v_cache.shape != k_cache.shape \
+    cache = (nb, hkv, BLOCK_TOKENS, d)
+    if out.shape != q.shape or k_cache.shape != cache or v_cache.shape != cache \
             or rows != B or seq_lens.shape != (B,) \
             or (k_new is not None and (k_new.shape != (B, hkv, d) or v_new.shape != (B, hkv, d))):
         raise ValueError("shape mismatch")
-    dev = _cuda_index(q, "q")
+    dev = q.get_device()
+    if dev < 0:
+        _not_one_device((q, "q"))
     bf, i32 = torch.bfloat16, torch.int32
     sin, sout, stride = _score_args(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS, dev)
     wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else
@@ -670,14 +669,17 @@ def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_l
     try:
         T, hq, d = q.shape
         B, W = block_tables.shape
-        nb, *tile = k_cache.shape
+        nb = k_cache.shape[0]
     except ValueError:
         raise ValueError("shape mismatch") from None
     hkv = num_kv_heads
-    if out.shape != q.shape or tile != [hkv, BLOCK_TOKENS, d] or v_cache.shape != k_cache.shape \
+    cache = (nb, hkv, BLOCK_TOKENS, d)
+    if out.shape != q.shape or k_cache.shape != cache or v_cache.shape != cache \
             or seq_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise ValueError("shape mismatch")
-    dev = _cuda_index(q, "q")
+    dev = q.get_device()
+    if dev < 0:
+        _not_one_device((q, "q"))
     bf, i32 = torch.bfloat16, torch.int32
     sin, sout, stride = _score_args(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS, dev)
     wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else _prefill_scored_bytes(
@@ -708,11 +710,13 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens
         ob, oh, ostride = scores_out.shape
     except ValueError:
         raise ValueError("shape mismatch") from None
-    if v_cache.shape != k_cache.shape or bt != BLOCK_TOKENS or rows != B or ib != B or ob != B \
+    if v_cache.shape != (nb, hkv, BLOCK_TOKENS, d) or bt != BLOCK_TOKENS or rows != B or ib != B or ob != B \
             or ih != hkv or oh != hkv or seq_lens.shape != (B,) or keep_lens.shape != (B,) \
             or kept.shape != (B, hkv, NW * BLOCK_TOKENS):
         raise ValueError("shape mismatch")
-    dev = _cuda_index(k_cache, "k_cache")
+    dev = k_cache.get_device()
+    if dev < 0:
+        _not_one_device((k_cache, "k_cache"))
     bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     _run(_lib.pkv_evict_tokens, "pkv_evict_tokens", dev,
          _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
