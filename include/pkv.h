@@ -475,7 +475,9 @@ PKV_API pkv_status pkv_paged_attention_decode_scored(
  *   scores_out[b][g][p] = (p < seq_lens[b] - rows_b ? scores_in[b][g][p] : 0)
  *                         + sum over the last min(window, rows_b) new tokens at positions >= p, and
  *                           the query heads h of KV head g, of their softmax weight on p
- * (window <= 0: every new token counts).  num_tokens: the rows of q and out
+ * (window <= 0: every new token counts).  Few rows over long contexts are cut
+ * along the keys and joined by log-sum-exp (same result up to fp32 rounding
+ * order); otherwise out has pkv_paged_attention_prefill's bits.  num_tokens: the rows of q and out
  * (query_start[num_seqs]).  scale > 0, at most 128 query heads per KV head.
  * A sequence with seq_lens[b] < its rows, past its table, with more than
  * max_query_len rows or rows past num_tokens is flagged PKV_DEV_ERR_BAD_LEN
@@ -486,7 +488,7 @@ PKV_API pkv_status pkv_paged_attention_decode_scored(
  * the same device current, else PKV_ERR_WORKSPACE.
  */
 PKV_API size_t pkv_prefill_scored_workspace_bytes(int num_tokens, int num_seqs, int max_query_len,
-                                                  int num_heads, int num_kv_heads,
+                                                  int num_heads, int num_kv_heads, int head_dim,
                                                   int max_blocks_per_seq, int window);
 PKV_API pkv_status pkv_paged_attention_prefill_scored(
     void *out, const void *q, int num_tokens, const void *k_cache, const void *v_cache,

@@ -132,12 +132,20 @@ struct PrefillParams {
     float *lse;
     int num_tokens;  // tokens of q that lse has room for
     int items;  // work items of the persistent tcgen05 kernel (set by its launcher)
+    // Optional (0 or 1: off; needs lse): each item's keys cut into key_parts
+    // ranges, their partial rows joined by a second kernel.
+    int key_parts;
+    float *part_o, *part_ml;  // [key_parts][num_tokens][Hq][D] and [..][2]
 };
 
 // On tcgen05 / TMEM: a persistent kernel, one CTA per SM, work items of two
 // 128-row Q tiles.
 cudaError_t launch_prefill_tc(const CUtensorMap &tmk, const CUtensorMap &tmv, const PrefillParams &p,
                               int head_dim, int max_query_len, int num_sms, cudaStream_t stream);
+
+// The key_parts for these sizes.
+int prefill_key_parts(int B, int Hq, int Hkv, int head_dim, int W, int max_query_len, int num_tokens,
+                      int num_sms);
 
 // The weights that the last `window` new tokens of each sequence put on its
 // tokens, from the prefill's log-sum-exp (pp.lse), added to the scores.

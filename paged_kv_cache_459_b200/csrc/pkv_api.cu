@@ -690,20 +690,27 @@ pkv_status pkv_paged_attention_prefill(void *out, const void *q, const void *k_c
 
 namespace {
 
-// The prefill scores' workspace: the rows' log-sum-exp, then the partial sums
-// when each unit's queries are cut into ranges.
+// The scored prefill's workspace: the rows' log-sum-exp, then the partial rows
+// when the attention's keys are cut into parts, then the partial sums when a
+// key tile's queries are cut into ranges.
 struct PrefillScoreWorkspace {
-    size_t partial, total;
-    int splits;
+    size_t part_o, part_ml, partial, total;
+    int splits, key_parts;
 };
 PrefillScoreWorkspace prefill_score_workspace(int num_tokens, int num_seqs, int max_query_len,
-                                              int num_heads, int num_kv_heads,
+                                              int num_heads, int num_kv_heads, int head_dim,
                                               int max_blocks_per_seq, int window) {
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     PrefillScoreWorkspace w;
     w.splits = pkv::prefill_score_splits(num_seqs, num_kv_heads, num_heads / num_kv_heads,
                                          max_blocks_per_seq, window, max_query_len, sm_count());
-    w.partial = up(static_cast<size_t>(num_tokens) * num_heads * sizeof(float));
+    w.key_parts = pkv::prefill_key_parts(num_seqs, num_heads, num_kv_heads, head_dim,
+                                         max_blocks_per_seq, max_query_len, num_tokens, sm_count());
+    const size_t rows = static_cast<size_t>(num_tokens) * num_heads;
+    const size_t part_rows = w.key_parts > 1 ? w.key_parts * rows : 0;
+    w.part_o = up(rows * sizeof(float));
+    w.part_ml = w.part_o + up(part_rows * head_dim * sizeof(float));
+    w.partial = w.part_ml + up(part_rows * 2 * sizeof(float));
     w.total = w.partial;
     if (w.splits > 1)
         w.total += up(static_cast<size_t>(w.splits) * num_seqs * num_kv_heads *
@@ -734,13 +741,13 @@ bool encode_q_map(CUtensorMap *m, const void *q, int num_tokens, int num_heads, 
 }  // namespace
 
 size_t pkv_prefill_scored_workspace_bytes(int num_tokens, int num_seqs, int max_query_len,
-                                          int num_heads, int num_kv_heads, int max_blocks_per_seq,
-                                          int window) {
+                                          int num_heads, int num_kv_heads, int head_dim,
+                                          int max_blocks_per_seq, int window) {
     if (num_tokens < 0 || num_seqs < 0 || max_query_len < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-        num_heads % num_kv_heads || max_blocks_per_seq <= 0)
+        num_heads % num_kv_heads || head_dim <= 0 || max_blocks_per_seq <= 0)
         return 0;
     return prefill_score_workspace(num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads,
-                                   max_blocks_per_seq, window_or_all(window)).total;
+                                   head_dim, max_blocks_per_seq, window_or_all(window)).total;
 }
 
 pkv_status pkv_paged_attention_prefill_scored(
@@ -770,7 +777,8 @@ pkv_status pkv_paged_attention_prefill_scored(
     if (score_stride < row_tokens) return PKV_ERR_INVALID_ARG;
     const int counted = window_or_all(window);
     const PrefillScoreWorkspace sw = prefill_score_workspace(
-        num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads, max_blocks_per_seq, counted);
+        num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+        counted);
     if (sw.total > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < sw.total))
         return PKV_ERR_WORKSPACE;
 
@@ -792,6 +800,9 @@ pkv_status pkv_paged_attention_prefill_scored(
     p.pp.scale_log2 = scale * 1.4426950408889634f;
     p.pp.lse = static_cast<float *>(workspace);
     p.pp.num_tokens = num_tokens;
+    p.pp.key_parts = sw.key_parts;
+    p.pp.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + sw.part_o);
+    p.pp.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + sw.part_ml);
     p.sp = pkv::ScoreParams{scores_in, scores_out, score_stride};
     p.splits = sw.splits;
     p.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + sw.partial);

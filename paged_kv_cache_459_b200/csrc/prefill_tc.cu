@@ -21,6 +21,7 @@
 // Every wait is bounded; on a timeout the kernel flags PKV_DEV_ERR_TIMEOUT,
 // stops issuing, and still frees its TMEM.
 #include <algorithm>
+#include <cmath>
 
 #include "decode_common.cuh"
 #include "tcgen05.cuh"
@@ -41,6 +42,7 @@ constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
 constexpr int kQWarp = kSoftmaxWarps + 2;  // + x: the Q rows of tile x
 constexpr int kThreads = (kSoftmaxWarps + 2 + kTiles) * 32;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kMaxKeyParts = 16;           // ranges an item's keys are cut into at most
 
 template <int D>
 struct TcGeometry {
@@ -68,13 +70,30 @@ struct TcGeometry {
 struct TcItem {
     int b, kvh, q0, ctx, rows, r_begin, first_pos, nblk_seq;
     int nk0, nk1;  // key tiles Q tile 0 / 1 can see (tile 1 may be empty: 0)
+    int ka, part;  // SPLIT: the part's first key tile (nk0, nk1 count from it), and which part it is
 };
+
+// Key tiles [ka, kb) of part `part` of nk.
+__device__ __forceinline__ void tc_part(int nk, int part, int parts, int &ka, int &kb) {
+    const int base = nk / parts, rem = nk - base * parts;
+    ka = part * base + min(part, rem);
+    kb = ka + base + (part < rem);
+}
 
 // Items are numbered z-major -- z counts 256-row tiles from the END of each
 // sequence, so low numbers see the most keys -- then sequence, then KV head.
 // Returns false for items past a sequence's rows or of a sequence whose
 // lengths are inconsistent (*bad set for the latter).
+// SPLIT: an item's key tiles are cut into p.key_parts ranges, a unit each, the
+// ranges of one item numbered side by side; false too for an empty range.
+template <bool SPLIT>
 __device__ __forceinline__ bool tc_item(const PrefillParams &p, int i, TcItem &it, bool *bad) {
+    it.ka = it.part = 0;
+    if (SPLIT) {
+        const int item = i / p.key_parts;
+        it.part = i - item * p.key_parts;
+        i = item;
+    }
     const int per_z = p.Hkv * p.B;
     const int z = i / per_z, rem = i - z * per_z;
     it.b = rem / p.Hkv;
@@ -94,6 +113,13 @@ __device__ __forceinline__ bool tc_item(const PrefillParams &p, int i, TcItem &i
     it.nk0 = (it.first_pos + last0 / p.group + kKeys) / kKeys;
     const int lo1 = it.r_begin + kRows;
     it.nk1 = lo1 < it.rows ? (it.first_pos + (min(it.rows, lo1 + kRows) - 1) / p.group + kKeys) / kKeys : 0;
+    if (SPLIT) {
+        int kb;
+        tc_part(max(it.nk0, it.nk1), it.part, p.key_parts, it.ka, kb);
+        it.nk0 = max(min(it.nk0, kb) - it.ka, 0);
+        it.nk1 = max(min(it.nk1, kb) - it.ka, 0);
+        if (it.nk0 == 0 && it.nk1 == 0) return false;
+    }
     return true;
 }
 
@@ -104,12 +130,13 @@ __device__ __forceinline__ int tc_item_index(int k, int c, int n) {
 }
 
 // Next valid item of this CTA at or after round k; returns its round or -1.
+template <bool SPLIT>
 __device__ __forceinline__ int tc_next_item(const PrefillParams &p, int k, TcItem &it) {
     for (;; ++k) {
         const int i = tc_item_index(k, blockIdx.x, gridDim.x);
         if (i >= p.items) return -1;
         bool bad;
-        if (tc_item(p, i, it, &bad)) return k;
+        if (tc_item<SPLIT>(p, i, it, &bad)) return k;
     }
 }
 
@@ -122,7 +149,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
 // barrier's phase runs on across items, and a dedicated warp fetches the next
 // item's Q rows (cp.async) as soon as the current item's last S product of
 // that Q tile is done.
-template <int D>
+// SPLIT (few items, long contexts): a unit is a range of an item's keys, and
+// its rows' unnormalised sums and (max, sum) go to the workspace.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv, const PrefillParams p) {
@@ -185,15 +214,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t policy = l2_policy_evict_normal();
             int gk = 0, gv = 0;  // K / V tiles loaded so far (ring position and phase)
             TcItem it, nx;
-            for (int k = tc_next_item(p, 0, it); k >= 0 && !*abort_flag; it = nx) {
-                const int kn = tc_next_item(p, k + 1, nx);
+            for (int k = tc_next_item<SPLIT>(p, 0, it); k >= 0 && !*abort_flag; it = nx) {
+                const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
                 const int32_t *trow = p.block_tables + static_cast<size_t>(it.b) * p.W;
                 const int nk = max(it.nk0, it.nk1);
                 for (int j = 0; j < nk && !*abort_flag; ++j) {
                     int y[kKeys / kBlockTokens];  // tensor-map rows of the tile's blocks
 #pragma unroll
                     for (int i = 0; i < kKeys / kBlockTokens; ++i) {
-                        const int blk = j * (kKeys / kBlockTokens) + i;
+                        const int blk = (it.ka + j) * (kKeys / kBlockTokens) + i;
                         long long yy = p.num_blocks * p.Hkv * kBlockTokens;  // past the tensor: zeros
                         if (blk < it.nblk_seq) {
                             const int32_t phys = __ldg(trow + blk);
@@ -247,10 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0;; ++k) {
                 const int i = tc_item_index(k, blockIdx.x, gridDim.x);
                 if (i >= p.items) break;
-                if (i < p.Hkv * p.B && i % p.Hkv == 0) {
+                const int item = SPLIT ? i / p.key_parts : i;
+                if (item < p.Hkv * p.B && item % p.Hkv == 0) {
                     TcItem bad_it;
                     bool bad;
-                    tc_item(p, i, bad_it, &bad);
+                    tc_item<SPLIT>(p, i, bad_it, &bad);
                     if (bad) flag(p.err, PKV_DEV_ERR_BAD_LEN);
                 }
             }
@@ -299,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ns[kTiles] = {0, 0};  // S products per Q tile (s_full / p_full phases)
         int n_it = 0;            // items done (q_full / o_done / o_free phases)
         TcItem it, nx;
-        int k = tc_next_item(p, 0, it);
+        int k = tc_next_item<SPLIT>(p, 0, it);
         for (; k >= 0 && ok; it = nx, ++n_it) {
             // the next item's parameters are read now, off the item boundary
-            const int kn = tc_next_item(p, k + 1, nx);
+            const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
             const int nk_t[kTiles] = {it.nk0, it.nk1};
             const int nk = max(it.nk0, it.nk1);
             wait(k_full(gk % KS), static_cast<uint32_t>((gk / KS) & 1));
@@ -324,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int sv = gv % VS;
                 wait(v_full(sv), static_cast<uint32_t>((gv / VS) & 1));
                 // V rows of slots at or past the sequence end may hold anything: zero them
-                const int k_lo = j * kKeys;
+                const int k_lo = (it.ka + j) * kKeys;
                 if (ok && k_lo + kKeys > it.ctx && k_lo < it.nblk_seq * kBlockTokens) {
                     const int z0 = max(it.ctx - k_lo, 0), z1 = min(it.nblk_seq * kBlockTokens - k_lo, kKeys);
                     uint8_t *vbase = smem + Geo::kV + sv * Geo::kKVBytes;
@@ -392,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int n_it = 0;
         TcItem it, nx;
-        for (int k = tc_next_item(p, 0, it); k >= 0 && ok; it = nx, ++n_it) {
-            const int kn = tc_next_item(p, k + 1, nx);
+        for (int k = tc_next_item<SPLIT>(p, 0, it); k >= 0 && ok; it = nx, ++n_it) {
+            const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
             {
                 if (n_it > 0 && (!mbar_wait(q_free(x), static_cast<uint32_t>((n_it - 1) & 1), kWaitLimitNs) ||
                                  *abort_flag)) {
@@ -439,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ns = 0;    // S products seen (s_full / p_full phases)
         int n_it = 0;  // items done (o_done phases)
         TcItem it, nx;  // the current and the next item
-        int k = tc_next_item(p, 0, it);
+        int k = tc_next_item<SPLIT>(p, 0, it);
         while (k >= 0 && ok) {
-            const int kn = tc_next_item(p, k + 1, nx);
+            const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
             const int r = it.r_begin + tile * kRows + t;
             const int row_pos = r < it.rows ? it.first_pos + r / G : -1;
             const int my_nk = tile == 0 ? it.nk0 : it.nk1;
@@ -458,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Two passes over S in TMEM, 64 columns at a time, so that a row
                 // never sits in registers whole (twelve warps leave 170 registers
                 // a thread): the row max first, then exp2 and P.
-                const int k0 = j * kKeys;
+                const int k0 = (it.ka + j) * kKeys;
                 const bool masked = __any_sync(0xffffffffu, k0 + kKeys - 1 > row_pos);
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1  // one half's 64 registers live at a time
@@ -566,6 +596,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 k = kn;
                 continue;
             }
+            if constexpr (SPLIT) {  // this part's unnormalised row and (max, sum)
+                const size_t row = (static_cast<size_t>(it.part) * p.num_tokens + it.q0 + r / G) * p.Hq + it.kvh * G + r % G;
+                const bool live = row_pos >= 0 && it.q0 >= 0 && it.q0 + r / G < p.num_tokens;
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    uint32_t o[32];
+                    tc::ld32(t_o + 32 * h, o);
+                    tc::wait_ld();
+                    if (live) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<uint4 *>(p.part_o + row * D + 32 * h + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                }
+                if (live) *reinterpret_cast<float2 *>(p.part_ml + 2 * row) = make_float2(m_run, l_run);
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_free(tile));
+                it = nx;
+                k = kn;
+                continue;
+            }
             // O row, normalised, packed to bf16 and stored 64 columns at a
             // time; then O_x is handed back
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
@@ -611,20 +663,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::dealloc<Geo::kTmemCols>(tmem);
 }
 
+// The parts of a row joined by log-sum-exp, in order: one warp a row.
+constexpr int kJoinWarps = 8;
+
 template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillParams p, long long rows_max) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const long long idx = static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const int q0 = __ldg(p.query_start + b), nq = __ldg(p.query_start + b + 1) - q0, ctx = __ldg(p.seq_lens + b);
+    if (idx >= rows_max || nq <= 0 || nq > rows_max / p.Hq || ctx < nq || ctx > p.W * kBlockTokens) return;
+    const int tok = static_cast<int>(idx / p.Hq), head = static_cast<int>(idx - static_cast<long long>(tok) * p.Hq);
+    if (tok >= nq || q0 < 0 || q0 + tok >= p.num_tokens) return;
+    const int kvh = head / p.group, r = tok * p.group + head % p.group, rows = nq * p.group;
+    // the key tiles of the row's Q tile and of its item, as tc_item counts them
+    const int first_pos = ctx - nq, tile_lo = r / kRows * kRows, item_lo = r / kCtaRows * kCtaRows;
+    const auto tiles_of = [&](int lo) { return (first_pos + (min(rows, lo + kRows) - 1) / p.group + kKeys) / kKeys; };
+    const int nk = tiles_of(tile_lo);
+    const int nk_item = item_lo + kRows < rows ? tiles_of(item_lo + kRows) : tiles_of(item_lo);
+    float M = -INFINITY, L = 0.f, o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.f;
+    for (int s = 0; s < p.key_parts; ++s) {
+        int ka, kb;
+        tc_part(nk_item, s, p.key_parts, ka, kb);
+        if (ka >= min(kb, nk)) continue;  // the part has no key of this row's tile: nothing was written
+        const size_t row = (static_cast<size_t>(s) * p.num_tokens + q0 + tok) * p.Hq + head;
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + 2 * row));
+        float x[V];
+        if constexpr (V == 4)
+            *reinterpret_cast<float4 *>(x) = __ldcg(reinterpret_cast<const float4 *>(p.part_o + row * D) + lane);
+        else
+            *reinterpret_cast<float2 *>(x) = __ldcg(reinterpret_cast<const float2 *>(p.part_o + row * D) + lane);
+        // a part whose keys all lie past the row (its tile's later rows see them) holds (-inf, 0)
+        const float m = fmaxf(M, ml.x);
+        const float a = M == -INFINITY ? 0.f : exp2f(M - m), c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+        L = L * a + ml.y * c;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = o[i] * a + (c == 0.f ? 0.f : x[i] * c);
+        M = m;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    __nv_bfloat16 *dst = p.out + (static_cast<size_t>(q0 + tok) * p.Hq + head) * D + lane * V;
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
+    if (lane == 0)
+        p.lse[(static_cast<size_t>(kvh) * p.num_tokens + q0) * p.group + r] = M + log2f(L);
+}
+
+template <int D, bool SPLIT>
 cudaError_t launch_prefill_tc_d(const CUtensorMap &tmk, const CUtensorMap &tmv, PrefillParams p,
                                 int max_query_len, int num_sms, cudaStream_t stream) {
     constexpr int kSmem = TcGeometry<D>::kSmemBytes;
-    auto kern = paged_prefill_tc_kernel<D>;
+    auto kern = paged_prefill_tc_kernel<D, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(max_query_len) * p.group;
-    const long long items = (rows + kCtaRows - 1) / kCtaRows * p.Hkv * p.B;
+    const long long items = (rows + kCtaRows - 1) / kCtaRows * p.Hkv * p.B * (SPLIT ? p.key_parts : 1);
     if (items == 0) return cudaSuccess;
     if (items > 0x7FFFFFFFLL - 2LL * num_sms) return cudaErrorInvalidValue;
     p.items = static_cast<int>(items);
     const unsigned grid = static_cast<unsigned>(std::min<long long>(items, num_sms));
     kern<<<grid, kThreads, kSmem, stream>>>(tmk, tmv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !SPLIT) return e;
+    const long long join_rows = static_cast<long long>(max_query_len) * p.Hq;
+    const long long ctas = (join_rows + kJoinWarps - 1) / kJoinWarps;
+    if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    prefill_join_kernel<D><<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p.B)), kJoinWarps * 32, 0, stream>>>(
+        p, join_rows);
     return cudaGetLastError();
 }
 
@@ -632,9 +741,41 @@ cudaError_t launch_prefill_tc_d(const CUtensorMap &tmk, const CUtensorMap &tmv, 
 
 cudaError_t launch_prefill_tc(const CUtensorMap &tmk, const CUtensorMap &tmv, const PrefillParams &p,
                               int head_dim, int max_query_len, int num_sms, cudaStream_t stream) {
-    if (head_dim == 128) return launch_prefill_tc_d<128>(tmk, tmv, p, max_query_len, num_sms, stream);
-    if (head_dim == 64) return launch_prefill_tc_d<64>(tmk, tmv, p, max_query_len, num_sms, stream);
+    if (p.key_parts > 1) {
+        if (head_dim == 128) return launch_prefill_tc_d<128, true>(tmk, tmv, p, max_query_len, num_sms, stream);
+        if (head_dim == 64) return launch_prefill_tc_d<64, true>(tmk, tmv, p, max_query_len, num_sms, stream);
+        return cudaErrorInvalidValue;
+    }
+    if (head_dim == 128) return launch_prefill_tc_d<128, false>(tmk, tmv, p, max_query_len, num_sms, stream);
+    if (head_dim == 64) return launch_prefill_tc_d<64, false>(tmk, tmv, p, max_query_len, num_sms, stream);
     return cudaErrorInvalidValue;
+}
+
+int prefill_key_parts(int B, int Hq, int Hkv, int head_dim, int W, int max_query_len, int num_tokens, int num_sms) {
+    // Only where the items do not give every SM one (30 new tokens after 10000, 2
+    // KV heads: 46 us a scored call against 235 uncut; one token after 12000, 8
+    // heads: 68 against 306).  With more, cutting the last, partly filled round
+    // gained nothing (224 items: 609 us against 611; 256: 217 against 213).
+    // Time in steps of one 128-key tile (two Q tiles against it): rounds of units
+    // over the SMs, each unit its steps and kUnit more (Q, the last step's mask,
+    // the epilogue), and the partials written and read.
+    constexpr double kUnit = 3.0;
+    constexpr double kStepBytes = 2.4e-6 * 4e12;  // what the join moves in a step's 2.4 us
+    const double rows = static_cast<double>(max_query_len) * (Hq / Hkv);
+    const double items = std::ceil(rows / kCtaRows) * Hkv * B;
+    if (items >= num_sms) return 1;
+    const int tiles = static_cast<int>((static_cast<long long>(W) * kBlockTokens + kKeys - 1) / kKeys);
+    double least = tiles + kUnit;
+    int parts = 1;
+    for (int n = 2; n <= kMaxKeyParts && n <= tiles; ++n) {
+        const double cost = std::ceil(items * n / num_sms) * (std::ceil(static_cast<double>(tiles) / n) + kUnit) + 2.0 +
+                            n * 2.0 * num_tokens * Hq * (head_dim + 2) * 4.0 / kStepBytes;
+        if (cost < 0.95 * least) {
+            least = cost;
+            parts = n;
+        }
+    }
+    return parts;
 }
 
 }  // namespace pkv

@@ -94,7 +94,7 @@ _sigs = {
     "pkv_paged_attention_decode_scored": ([_P, _P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32,
                                            _i32, _i64, _f32, _P, _P, _i64, _i32, _i32, _P, _sz, _P,
                                            _P], _i32),
-    "pkv_prefill_scored_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
+    "pkv_prefill_scored_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
     "pkv_paged_attention_prefill_scored": ([_P, _P, _i32, _P, _P, _P, _i32, _P, _P, _i32, _i32,
                                             _i32, _i32, _i32, _i64, _f32, _P, _P, _i64, _i32, _P,
                                             _sz, _P, _P], _i32),
@@ -644,7 +644,7 @@ def _prefill_scored_bytes(dev, *sizes) -> int:
 
 
 def prefill_scored_workspace_bytes(num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads,
-                                   max_blocks_per_seq, window=0, device=None) -> int:
+                                   head_dim, max_blocks_per_seq, window=0, device=None) -> int:
     """Workspace of paged_attention_prefill_scored for these sizes on a CUDA device (default: the
     current one)."""
     import torch
@@ -654,7 +654,7 @@ def prefill_scored_workspace_bytes(num_tokens, num_seqs, max_query_len, num_head
     else:
         dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     return _prefill_scored_bytes(-1 if dev is None else dev, num_tokens, num_seqs, max_query_len,
-                                 num_heads, num_kv_heads, max_blocks_per_seq, window)
+                                 num_heads, num_kv_heads, head_dim, max_blocks_per_seq, window)
 
 
 def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, scale,
@@ -683,7 +683,7 @@ def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_l
     bf, i32 = torch.bfloat16, torch.int32
     sin, sout, stride = _score_args(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS, dev)
     wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else _prefill_scored_bytes(
-        dev, T, B, max_query_len, hq, hkv, W, window))
+        dev, T, B, max_query_len, hq, hkv, d, W, window))
     _run(_lib.pkv_paged_attention_prefill_scored, "pkv_paged_attention_prefill_scored", dev,
          _ptr(out, bf, "out", dev), _ptr(q, bf, "q", dev), T,
          _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),

@@ -37,6 +37,18 @@ def weights(q, k, scale, pos):
     return e / e.sum(1, keepdims=True)
 
 
+def attention(q, query_start, k_cache, v_cache, tables, lens, scale):
+    """[T, Hq, d]: each new token's attention over the tokens up to its own."""
+    out = np.zeros(q.shape)
+    g = q.shape[1] // k_cache.shape[1]
+    for b, n in enumerate(lens):
+        lo, hi = int(query_start[b]), int(query_start[b + 1])
+        for m in range(q.shape[1] if hi > lo else 0):
+            w = weights(q[lo:hi, m], rows(k_cache, tables[b], n, m // g), scale, np.arange(n - (hi - lo), n))
+            out[lo:hi, m] = w @ rows(v_cache, tables[b], n, m // g)
+    return out
+
+
 def scores(q, query_start, k_cache, tables, lens, scale, scores_in, window=0):
     """[B, Hkv, S] accumulated weights, NaN where nothing is written.  q [T, Hq, d] and the caches
     as float64; sequence b's new tokens are q rows query_start[b] .. query_start[b + 1]."""

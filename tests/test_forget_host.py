@@ -104,8 +104,8 @@ def test_scored_workspace_sizes():
     assert pkv.decode_scored_workspace_bytes(1, 2, 2, 64, 1) >= 2 * 16 * 4 + 8
     assert pkv.decode_scored_workspace_bytes(2, 24, 2, 64, 5) >= 2 * 2 * 2 * 8 * 80 * 4
     assert pkv.decode_scored_workspace_bytes(2, 5, 2, 64, 5) == 0
-    assert pkv.prefill_scored_workspace_bytes(-1, 2, 16, 4, 2, 8) == 0
-    assert pkv.prefill_scored_workspace_bytes(20, 2, 16, 4, 2, 8) >= 20 * 4 * 4
+    assert pkv.prefill_scored_workspace_bytes(-1, 2, 16, 4, 2, 64, 8) == 0
+    assert pkv.prefill_scored_workspace_bytes(20, 2, 16, 4, 2, 64, 8) >= 20 * 4 * 4
 
 
 def _same(a, m):

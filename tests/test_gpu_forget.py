@@ -276,7 +276,7 @@ def test_scored_decode_lengths_past_the_table():
 
 # ------------------------------------------------------------------ scored prefill
 
-def prefill_case(new, old, hq, hkv, d, window=0, with_old=True, seed=0, width=None, scale=None):
+def prefill_case(new, old, hq, hkv, d, window=0, with_old=True, seed=0, width=None, scale=None, whole=False):
     B = len(new)
     lens = [a + b for a, b in zip(new, old)]
     tables, pool, _ = tables_for(lens, seed, width=width)
@@ -300,8 +300,12 @@ def prefill_case(new, old, hq, hkv, d, window=0, with_old=True, seed=0, width=No
     if T:
         pkv.paged_attention_prefill(out2, q, kc, vc, t, ln, st, scale, hkv, max(new))
     assert int(err.item()) == 0
-    assert same_bits(out, out2)
+    if whole:  # keys not cut into parts
+        assert same_bits(out, out2)
     q64, k64 = f64(q), f64(kc)
+    if T:
+        want_out = ref.attention(q64, qs, k64, f64(vc), tables, lens, scale)
+        check_close(out.view(torch.int16).cpu().numpy().view(np.uint16), want_out, "prefill")
     before = old_scores.astype(np.float64) if with_old else np.zeros(old_scores.shape)
     want = ref.scores(q64, qs, k64, tables, lens, scale, before, window)
     got = f64(sout)
@@ -323,8 +327,18 @@ def test_scored_prefill(new, old, hq, hkv, d, window):
 
 
 def test_scored_prefill_unsplit_units():
-    """Enough (sequence, head, key tile) units that no unit's queries are cut into ranges."""
-    prefill_case([300] * 20, [0] * 20, 32, 32, 64, seed=4)
+    """Enough (sequence, head, key tile) units that no unit's queries are cut into ranges, and enough
+    items that no item's keys are cut into parts: the bits of the call without scores."""
+    prefill_case([300] * 20, [0] * 20, 32, 32, 64, seed=4, whole=True)
+
+
+@pytest.mark.parametrize("new,old,hq,hkv,d", [
+    ([5], [4000], 4, 1, 64), ([129, 1, 0], [3000, 2500, 100], 8, 2, 128), ([300, 40], [1500, 1700], 14, 2, 64),
+    ([257], [2300], 12, 1, 128), ([64, 700], [0, 2000], 6, 2, 64), ([1], [130], 3, 3, 128), ([33], [6000], 40, 1, 64),
+])
+def test_scored_prefill_keys_cut_into_parts(new, old, hq, hkv, d):
+    """Few rows over long contexts: parts of every length, some past a tile's or a row's keys."""
+    prefill_case(new, old, hq, hkv, d, window=16, seed=sum(new))
 
 
 def test_scored_prefill_table_wider_than_the_sequences():
