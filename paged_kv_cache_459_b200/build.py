@@ -1,4 +1,5 @@
-"""Build ``libpkv.so`` in-tree with nvcc for sm_100a (B200).
+"""Build ``libpkv.so`` in-tree with nvcc for sm_100a (B200), and ``_marshal.so``, the
+argument marshalling of some of the Python binding's calls, with the host compiler.
 
     python -m paged_kv_cache_459_b200.build [--force] [--verbose-ptxas]
 
@@ -12,11 +13,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpkv.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -41,7 +45,20 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    deps = [MARSHAL_SRC, os.path.join(ROOT, "include", "pkv.h")]
+    if not force and os.path.exists(MARSHAL) \
+            and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
+        return MARSHAL
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    subprocess.run(["gcc", "-O2", "-std=gnu11", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wextra",
+                    "-I", sysconfig.get_paths()["include"], "-o", tmp, MARSHAL_SRC], check=True)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_marshal(force)
     if not force and not _stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.pp.group;
     const int rows = p.tile_tokens * G;  // rows a Q box fills
+    pdl_launch_dependents();  // the join's CTAs may take their places; they wait for this grid
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -465,9 +466,11 @@ constexpr int kJoinThreads = 256;
 
 // The splits' sums, in order.
 __global__ void __launch_bounds__(kJoinThreads) prefill_scores_join_kernel(const PrefillScoreParams p) {
+    pdl_launch_dependents();
     const int b = blockIdx.y / p.pp.Hkv;
     const size_t row = blockIdx.y;
     const int pos = blockIdx.x * kJoinThreads + threadIdx.x;
+    pdl_wait_primary();
     ScoreSeq sq;
     if (!score_seq(p, b, sq) || pos >= sq.ctx) return;
     const size_t tokens = static_cast<size_t>(p.pp.W) * kBlockTokens;
@@ -495,8 +498,7 @@ cudaError_t launch_d(const CUtensorMap &tmk, const CUtensorMap &tmq, PrefillScor
     if (e != cudaSuccess || p.splits == 1) return e;
     const dim3 jgrid(static_cast<unsigned>((tokens + kJoinThreads - 1) / kJoinThreads),
                      static_cast<unsigned>(p.pp.B * p.pp.Hkv));
-    prefill_scores_join_kernel<<<jgrid, kJoinThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(prefill_scores_join_kernel, jgrid, dim3(kJoinThreads), stream, p);
 }
 
 }  // namespace

@@ -101,7 +101,8 @@ __device__ __forceinline__ bool tc_item(const PrefillParams &p, int i, TcItem &i
     it.q0 = __ldg(p.query_start + it.b);
     const int nq = __ldg(p.query_start + it.b + 1) - it.q0;
     it.ctx = __ldg(p.seq_lens + it.b);
-    *bad = nq > 0 && (it.ctx < nq || it.ctx > p.W * kBlockTokens);
+    *bad = nq > 0 && (it.ctx < nq || it.ctx > p.W * kBlockTokens ||
+                      (p.lse != nullptr && (it.q0 < 0 || nq > p.num_tokens - it.q0)));
     if (nq <= 0 || *bad) return false;
     it.rows = nq * p.group;
     const int ntile = (it.rows + kCtaRows - 1) / kCtaRows;

@@ -21,10 +21,14 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "pkv.h")
 
-if not os.path.exists(LIB_PATH):
+_MARSHAL_PATH = os.path.join(_HERE, "_marshal.so")
+
+if not os.path.exists(LIB_PATH) or not os.path.exists(_MARSHAL_PATH):
     raise ImportError(
-        f"{LIB_PATH} is missing: build it with `python -m paged_kv_cache_459_b200.build` "
+        f"{LIB_PATH if not os.path.exists(LIB_PATH) else _MARSHAL_PATH} is missing: build it with `python -m paged_kv_cache_459_b200.build` "
         "(nvcc, sm_100a). There is no CPU fallback.")
+
+from . import _marshal  # noqa: E402
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -159,27 +163,55 @@ def _stream_ptr(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _ptr(t, dtype, name, dev: int) -> int:
-    """_dev_tensor for the calls whose tensors must all be on device `dev`: four tensor
-    methods a tensor, since a small call's time is its argument marshalling."""
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _dev_tensor(t, dtype, name)  # says what is wrong
+# The calls that _marshal makes: their tensors' types are checked there (csrc/marshal.c),
+# shapes and sizes here.  For each, its address and the names of its arguments.
+_MARSHALLED = []
+_DTYPES: list = []
+
+
+def _marshalled(symbol, names) -> int:
+    fn = getattr(_lib, symbol)
+    _MARSHALLED.append((symbol, ctypes.cast(fn, ctypes.c_void_p).value, names.split()))
+    return len(_MARSHALLED) - 1
+
+
+_ROPE = _marshalled("pkv_rope_kv_write", "q_out:b q:b k:b v:b . . . . k_cache:b v_cache:b slot_mapping:l "
+                    "positions:i . . cos_sin:f . . . . . . . . err:i")
+_DECODE = _marshalled("pkv_paged_attention_decode_scored", "out:b q:b k_new:b v_new:b k_cache:b v_cache:b "
+                      "block_tables:i . seq_lens:i . . . . . . scores_in:f scores_out:f . . . . . err:i")
+_PREFILL = _marshalled("pkv_paged_attention_prefill_scored", "out:b q:b . k_cache:b v_cache:b block_tables:i . "
+                       "seq_lens:i query_start:i . . . . . . . scores_in:f scores_out:f . . . . err:i")
+_EVICT = _marshalled("pkv_evict_tokens", "k_cache:b v_cache:b block_tables:i . seq_lens:i new_tables:i . "
+                     "keep_lens:i scores_in:f . scores_out:f . kept:i . . . . . . err:i")
+
+
+def _bad_argument(which, i, t):
+    """Says what is wrong with tensor argument i of a marshalled call."""
+    import torch
+
+    name, letter = _MARSHALLED[which][2][i].split(":")
+    _dev_tensor(t, dict(b=torch.bfloat16, i=torch.int32, l=torch.int64, f=torch.float32)[letter], name)
     raise ValueError(f"{name}: tensors must be on one device")
 
 
-def _run(fn, name, dev: int, *args) -> None:
-    """fn(*args, stream) on device `dev`'s current stream, with that device current."""
+def _run(which, dev: int, *args) -> None:
+    """A marshalled call on device `dev`'s current stream, with that device current."""
     import torch
 
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
-        code = fn(*args, stream)
+    if not _DTYPES:
+        _marshal.setup(torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8)
+        _DTYPES.append(True)
+    if dev < 0:  # not a CUDA tensor
+        code = -1
+    elif dev == torch._C._cuda_getDevice():
+        code = _marshal.call(which, _MARSHALLED[which][1], dev, *args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, stream)
+            code = _marshal.call(which, _MARSHALLED[which][1], dev, *args, torch._C._cuda_getCurrentRawStream(dev))
     if code != OK:
-        raise PkvError(code, name)
+        if code < 0:
+            _bad_argument(which, -code - 1, args[-code - 1])
+        raise PkvError(code, _MARSHALLED[which][0])
 
 
 def paged_kv_write(k, v, k_cache, v_cache, slot_mapping, err=None) -> None:
@@ -483,37 +515,27 @@ def suffix_blocks_bound(seq_lens, prefix_blocks) -> int:
 
 
 # ------------------------------------------- rotary write, scores, eviction
-def _not_one_device(*named):
-    """Raises what is wrong with tensors of which some are not on the first one's CUDA device."""
-    for t, name in named:
-        if t is not None and t.device.type != "cuda":
-            raise ValueError(f"{name} must be on a CUDA device")
-    raise ValueError("tensors must be on one device")
-
-
 def _scratch(dev, workspace, nbytes):
     """(pointer, bytes, tensor) of a call's workspace: the caller's, or one of the call's own
     from torch's allocator (ordered with the stream; inside a graph capture the graph's own)."""
     import torch
 
     if workspace is None:
+        if dev < 0:
+            return 0, 0, None  # not a CUDA call: refused with its tensors
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
         return workspace.data_ptr(), nbytes, workspace
-    return _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel(), workspace
+    if workspace.get_device() != dev:
+        raise ValueError("workspace: tensors must be on one device")
+    return _dev_tensor(workspace, torch.uint8, "workspace"), workspace.numel(), workspace
 
 
-def _token_rows(t, name, heads, d, dev):
-    """Pointer and token stride of a [T, heads, d] bf16 tensor whose rows are contiguous."""
-    import torch
-
+def _token_stride(t, name, heads, d):
+    """Token stride of a [T, heads, d] tensor whose rows are contiguous."""
     st, sh, sd = t.stride()
-    if t.dtype is torch.bfloat16 and t.get_device() == dev and sd == 1 and (sh == d or heads == 1):
-        return t.data_ptr(), st
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        _not_one_device((t, name))
-    raise ValueError(f"{name}: each token's heads must be contiguous")
+    if sd != 1 or (sh != d and heads != 1):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return st
 
 
 def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, *,
@@ -543,23 +565,13 @@ def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != rot // 2:
             raise ValueError("pair_axis: one axis for each of the rot / 2 pairs")
-    dev = q.get_device()
-    if dev < 0:
-        _not_one_device((q, "q"))
-    qop, qos = _token_rows(q_out, "q_out", hq, d, dev)
-    qp, qs = _token_rows(q, "q", hq, d, dev)
-    kp, ks = _token_rows(k, "k", hkv, d, dev)
-    vp, vs = _token_rows(v, "v", hkv, d, dev)
+    qos, qs = _token_stride(q_out, "q_out", hq, d), _token_stride(q, "q", hq, d)
+    ks, vs = _token_stride(k, "k", hkv, d), _token_stride(v, "v", hkv, d)
     if T == 1:  # a single row's stride says nothing
         qos = qs = hq * d
         ks = vs = hkv * d
-    bf = torch.bfloat16
-    _run(_lib.pkv_rope_kv_write, "pkv_rope_kv_write", dev, qop, qp, kp, vp, qos, qs, ks, vs,
-         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
-         _ptr(slot_mapping, torch.int64, "slot_mapping", dev),
-         _ptr(positions, torch.int32, "positions", dev), axes, pair_axis,
-         _ptr(cos_sin, torch.float32, "cos_sin", dev), max_positions, rot, interleaved, T, hq, hkv, d,
-         nb, None if err is None else _ptr(err, torch.int32, "err", dev))
+    _run(_ROPE, q.get_device(), q_out, q, k, v, qos, qs, ks, vs, k_cache, v_cache, slot_mapping, positions, axes,
+         pair_axis, cos_sin, max_positions, rot, interleaved, T, hq, hkv, d, nb, err)
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -579,16 +591,12 @@ def decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, m
                                                       max_blocks_per_seq, partition_tokens))
 
 
-def _score_args(scores_in, scores_out, B, hkv, tokens, dev):
-    import torch
-
+def _score_stride(scores_in, scores_out, B, hkv, tokens) -> int:
     stride = scores_out.shape[-1]
     rows = (B, hkv, stride)
     if scores_out.shape != rows or stride < tokens or (scores_in is not None and scores_in.shape != rows):
         raise ValueError("scores: [B, Hkv, at least the table's tokens], in and out alike")
-    f32 = torch.float32
-    return (None if scores_in is None else _ptr(scores_in, f32, "scores_in", dev),
-            _ptr(scores_out, f32, "scores_out", dev), stride)
+    return stride
 
 
 def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_lens, scale, num_kv_heads,
@@ -616,21 +624,12 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
             or rows != B or seq_lens.shape != (B,) \
             or (k_new is not None and (k_new.shape != (B, hkv, d) or v_new.shape != (B, hkv, d))):
         raise ValueError("shape mismatch")
+    stride = _score_stride(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS)
     dev = q.get_device()
-    if dev < 0:
-        _not_one_device((q, "q"))
-    bf, i32 = torch.bfloat16, torch.int32
-    sin, sout, stride = _score_args(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS, dev)
     wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else
                              decode_scored_workspace_bytes(B, hq, hkv, d, W, partition_tokens))
-    _run(_lib.pkv_paged_attention_decode_scored, "pkv_paged_attention_decode_scored", dev,
-         _ptr(out, bf, "out", dev), _ptr(q, bf, "q", dev),
-         None if k_new is None else _ptr(k_new, bf, "k_new", dev),
-         None if v_new is None else _ptr(v_new, bf, "v_new", dev),
-         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
-         _ptr(block_tables, i32, "block_tables", dev), W, _ptr(seq_lens, i32, "seq_lens", dev), B, hq,
-         hkv, d, nb, scale, sin, sout, stride, variant, partition_tokens, wp, wn,
-         None if err is None else _ptr(err, i32, "err", dev))
+    _run(_DECODE, dev, out, q, k_new, v_new, k_cache, v_cache, block_tables, W, seq_lens, B, hq, hkv, d, nb, scale,
+         scores_in, scores_out, stride, variant, partition_tokens, wp, wn, err)
 
 
 @lru_cache(maxsize=256)
@@ -677,19 +676,12 @@ def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_l
     if out.shape != q.shape or k_cache.shape != cache or v_cache.shape != cache \
             or seq_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise ValueError("shape mismatch")
+    stride = _score_stride(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS)
     dev = q.get_device()
-    if dev < 0:
-        _not_one_device((q, "q"))
-    bf, i32 = torch.bfloat16, torch.int32
-    sin, sout, stride = _score_args(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS, dev)
     wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else _prefill_scored_bytes(
         dev, T, B, max_query_len, hq, hkv, d, W, window))
-    _run(_lib.pkv_paged_attention_prefill_scored, "pkv_paged_attention_prefill_scored", dev,
-         _ptr(out, bf, "out", dev), _ptr(q, bf, "q", dev), T,
-         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
-         _ptr(block_tables, i32, "block_tables", dev), W, _ptr(seq_lens, i32, "seq_lens", dev),
-         _ptr(query_start, i32, "query_start", dev), B, max_query_len, hq, hkv, d, nb, scale, sin, sout,
-         stride, window, wp, wn, None if err is None else _ptr(err, i32, "err", dev))
+    _run(_PREFILL, dev, out, q, T, k_cache, v_cache, block_tables, W, seq_lens, query_start, B, max_query_len, hq,
+         hkv, d, nb, scale, scores_in, scores_out, stride, window, wp, wn, err)
 
 
 def evict_tokens(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens, scores_in, scores_out,
@@ -714,17 +706,8 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, new_tables, keep_lens
             or ih != hkv or oh != hkv or seq_lens.shape != (B,) or keep_lens.shape != (B,) \
             or kept.shape != (B, hkv, NW * BLOCK_TOKENS):
         raise ValueError("shape mismatch")
-    dev = k_cache.get_device()
-    if dev < 0:
-        _not_one_device((k_cache, "k_cache"))
-    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    _run(_lib.pkv_evict_tokens, "pkv_evict_tokens", dev,
-         _ptr(k_cache, bf, "k_cache", dev), _ptr(v_cache, bf, "v_cache", dev),
-         _ptr(block_tables, i32, "block_tables", dev), W, _ptr(seq_lens, i32, "seq_lens", dev),
-         _ptr(new_tables, i32, "new_tables", dev), NW, _ptr(keep_lens, i32, "keep_lens", dev),
-         _ptr(scores_in, f32, "scores_in", dev), istride, _ptr(scores_out, f32, "scores_out", dev),
-         ostride, _ptr(kept, i32, "kept", dev), sink, recent, B, hkv, d, nb,
-         None if err is None else _ptr(err, i32, "err", dev))
+    _run(_EVICT, k_cache.get_device(), k_cache, v_cache, block_tables, W, seq_lens, new_tables, NW, keep_lens,
+         scores_in, istride, scores_out, ostride, kept, sink, recent, B, hkv, d, nb, err)
 
 
 # ---------------------------------------------------------------- allocator

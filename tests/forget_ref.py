@@ -31,10 +31,14 @@ def rows(cache, table, n, h):
 def weights(q, k, scale, pos):
     """Softmax weights [rows, keys] of query rows q at positions pos over keys 0 .. len(k) - 1."""
     x = (q @ k.T) * scale
-    x[np.arange(k.shape[0])[None] > np.asarray(pos)[:, None]] = -np.inf
+    unseen = np.arange(k.shape[0])[None] > np.asarray(pos)[:, None]
+    x[unseen] = -np.inf
     x -= x.max(1, keepdims=True)
     e = np.exp(x)
-    return e / e.sum(1, keepdims=True)
+    e[unseen] = 0.0
+    w = e / e.sum(1, keepdims=True)
+    w[unseen] = 0.0  # no weight, whatever the seen ones hold
+    return w
 
 
 def attention(q, query_start, k_cache, v_cache, tables, lens, scale):

@@ -212,3 +212,56 @@ def test_rope_table_is_the_cosines_and_sines_of_the_positions():
     assert abs(float(t[p, i]) - np.cos(ang)) <= 2.0 ** -24 + 1e-11
     assert abs(float(t[p, 32 + i]) - np.sin(ang)) <= 2.0 ** -24 + 1e-11
     assert ctypes.sizeof(ctypes.c_float) == 4
+
+
+def test_marshalled_arguments_are_the_headers():
+    """marshal.c's letter for every argument of the four calls fits the header's declaration, and
+    the binding's names stand at the tensors."""
+    import re
+
+    src = open(pkv_build.MARSHAL_SRC).read()
+    header = re.sub(r"/\*.*?\*/", "", open(pkv.HEADER).read(), flags=re.S)
+    found = re.findall(r'"(\w+)", */\* (pkv_\w+) \*/', src)
+    assert [name for _, name in found] == [m[0] for m in pkv._MARSHALLED]
+    kinds = dict(b="void", r="void", p="void", i="int32_t", l="int64_t", f="float", s="uint8_t")
+    for (spec, name), (_, address, names) in zip(found, pkv._MARSHALLED):
+        args = [a.strip() for a in re.search(r"%s\((.*?)\);" % name, header, re.S).group(1).replace("\n", " ").split(",")]
+        assert len(args) == len(spec) == len(names) + 1 and address
+        for c, arg, n in zip(spec, args, names + ["."]):
+            if c in "nqx":
+                assert "*" not in arg or "stream" in arg
+                assert {"n": "int ", "q": "int64_t ", "x": "float "}[c] in arg or "size_t" in arg or "stream" in arg
+                assert n == "."
+                continue
+            assert "*" in arg and (kinds[c.lower()] in arg or arg == "unsigned int *err_word"), (c, arg)
+            assert (n == ".") == (c in "sp")
+            if n != ".":
+                assert arg.endswith("*" + dict(tables="x").get(n.split(":")[0], n.split(":")[0])) or n.startswith("err")
+                assert n.split(":")[1] == dict(r="b").get(c.lower(), c.lower())
+
+
+def test_marshal_refuses_what_it_cannot_convert():
+    from paged_kv_cache_459_b200 import _marshal
+    import torch
+
+    _marshal.setup(torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8)
+    with pytest.raises(TypeError):
+        _marshal.call(9, 1, 0)
+    with pytest.raises(TypeError):
+        _marshal.call(3, 1, 0, 1, 2)
+    t, i, s = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 1, 16)
+    address = pkv._MARSHALLED[pkv._EVICT][1]
+    args = [t, t, i, 1, i, i, 1, i, s, 16, s, 16, i, 0, 0, 1, 1, 64, 2, None, 0]
+    # host tensors stand for device -1; every tensor's type, device and layout is looked at
+    for at, bad in ((0, t.float()), (0, 5), (2, i.long()), (8, s.double()), (12, "kept"), (1, t.transpose(0, 1).expand(2, 2, 16, 64))):
+        a = list(args)
+        a[at] = bad
+        assert _marshal.call(pkv._EVICT, address, -1, *a) == -(at + 1)
+    assert _marshal.call(pkv._EVICT, address, 0, *args) == -1     # another device
+    for at, bad, error in ((3, 1 << 40, OverflowError), (3, "w", TypeError), (18, 1 << 70, OverflowError)):
+        a = list(args)
+        a[at] = bad
+        with pytest.raises(error):
+            _marshal.call(pkv._EVICT, address, -1, *a)
+    # the same tables before and after: the library's own check answers
+    assert _marshal.call(pkv._EVICT, address, -1, *args) == pkv.ERR_INVALID_ARG

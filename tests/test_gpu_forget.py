@@ -392,6 +392,58 @@ def test_scored_prefill_flags_what_does_not_fit():
     assert int(err.item()) == pkv.DEV_ERR_BAD_BLOCK and same_bits(sout[1:], good[1:])
 
 
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (14, 2), (2, 2)])
+def test_scores_of_infinities_and_nan(hq, hkv):
+    """An infinity in a key, or NaN in a query or a key, goes where the formula takes it: every weight
+    of the rows it meets, and no other row's."""
+    d, n, scale = 64, 300, 0.125
+    tables, pool, _ = tables_for([n, n], 1)
+    for what in ("q", "nan", "inf"):
+        kc, vc, q = normal((pool, hkv, BT, d), 1), normal((pool, hkv, BT, d), 2), normal((2 * n, hq, d), 3)
+        if what == "q":
+            q[200, 1, 3] = NAN          # sequence 0, token 200, query head 1
+        else:
+            kc[int(tables[0, 250 // BT]), 0, 250 % BT, 5] = NAN if what == "nan" else float("inf")
+        i32 = lambda *x: cuda(np.array(x, np.int32))  # noqa: E731
+        sout, out = torch.zeros((2, hkv, tables.shape[1] * BT), device="cuda"), torch.empty_like(q)
+        pkv.paged_attention_prefill_scored(out, q, kc, vc, cuda(tables), i32(n, n), i32(0, n, 2 * n), scale, hkv, n, sout)
+        q64, k64 = f64(q), f64(kc)
+        with np.errstate(all="ignore"):
+            want = ref.scores(q64, [0, n, 2 * n], k64, tables, [n, n], scale, None)
+        got = f64(sout)[:, :, :n]
+        want = want[:, :, :n]
+        assert np.isnan(want).any() and not np.isnan(want).all()
+        assert np.array_equal(np.isnan(got), np.isnan(want)), what
+        fine = ~np.isnan(want)
+        assert (np.abs(got - want)[fine] <= 1e-3 * want[fine]).all()
+        # the same rows one at a time, as decode steps see them
+        rows = np.array([[199, 250], [200, 251], [n - 1, n - 1]])
+        for pair in rows:
+            sout.zero_()
+            o = torch.empty((2, hq, d), dtype=BF, device="cuda")
+            pkv.paged_attention_decode_scored(o, torch.stack([q[pair[0]], q[n + pair[1]]]).contiguous(), kc, vc, cuda(tables),
+                                              i32(pair[0] + 1, pair[1] + 1), scale, hkv, sout)
+            with np.errstate(all="ignore"):
+                want1 = ref.scores(np.stack([q64[pair[0]], q64[n + pair[1]]]), [0, 1, 2], k64, tables, pair + 1, scale, None)
+            got1 = f64(sout)
+            for b in range(2):
+                assert np.array_equal(np.isnan(got1[b, :, :pair[b] + 1]), np.isnan(want1[b, :, :pair[b] + 1])), (what, pair, b)
+
+
+def test_scored_prefill_rows_past_the_queries():
+    """query_start past the rows of q: the sequence is flagged and left out, nothing of it is read or written."""
+    hq, hkv, d = 4, 2, 64
+    tables, pool, _ = tables_for([20, 40], 1)
+    kc, vc, q = normal((pool, hkv, BT, d), 1), normal((pool, hkv, BT, d), 2), normal((64, hq, d), 3)
+    out = torch.full((64, hq, d), NAN, dtype=BF, device="cuda")
+    sout, err = torch.full((2, hkv, tables.shape[1] * BT), -7.0, device="cuda"), new_err()
+    pkv.paged_attention_prefill_scored(out[:50], q[:50], kc, vc, cuda(tables), cuda(np.array([20, 40], np.int32)),
+                                       cuda(np.array([0, 20, 60], np.int32)), 0.125, hkv, 40, sout, err=err)
+    assert int(err.item()) == pkv.DEV_ERR_BAD_LEN
+    assert out[:20].isfinite().all() and out[20:].isnan().all()
+    assert (sout[0, :, :20] > 0).all() and (sout[1] == -7).all()
+
+
 # ------------------------------------------------------------------ eviction
 
 def evict_case(lens, keep, hkv, d, sink, recent, scores=None, seed=0, width=None):
