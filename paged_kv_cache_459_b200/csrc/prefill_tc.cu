@@ -66,11 +66,16 @@ struct TcGeometry {
     static_assert(kO + kTiles * D <= kTmemCols, "tensor memory columns");
 };
 
+// What a launch does beside the attention's rows: nothing; each row's
+// log-sum-exp; or (few items, long contexts) an item's keys cut into parts, whose
+// unnormalised rows a second kernel joins.
+constexpr int kPlain = 0, kLse = 1, kSplit = 2;
+
 // One work item: 256 query rows (two Q tiles) of one (sequence, KV head).
 struct TcItem {
     int b, kvh, q0, ctx, rows, r_begin, first_pos, nblk_seq;
     int nk0, nk1;  // key tiles Q tile 0 / 1 can see (tile 1 may be empty: 0)
-    int ka, part;  // SPLIT: the part's first key tile (nk0, nk1 count from it), and which part it is
+    int ka, part;  // kSplit: the part's first key tile (nk0, nk1 count from it), and which part it is
 };
 
 // Key tiles [ka, kb) of part `part` of nk.
@@ -84,12 +89,12 @@ __device__ __forceinline__ void tc_part(int nk, int part, int parts, int &ka, in
 // sequence, so low numbers see the most keys -- then sequence, then KV head.
 // Returns false for items past a sequence's rows or of a sequence whose
 // lengths are inconsistent (*bad set for the latter).
-// SPLIT: an item's key tiles are cut into p.key_parts ranges, a unit each, the
+// kSplit: an item's key tiles are cut into p.key_parts ranges, a unit each, the
 // ranges of one item numbered side by side; false too for an empty range.
-template <bool SPLIT>
+template <int MODE>
 __device__ __forceinline__ bool tc_item(const PrefillParams &p, int i, TcItem &it, bool *bad) {
     it.ka = it.part = 0;
-    if (SPLIT) {
+    if constexpr (MODE == kSplit) {
         const int item = i / p.key_parts;
         it.part = i - item * p.key_parts;
         i = item;
@@ -101,8 +106,8 @@ __device__ __forceinline__ bool tc_item(const PrefillParams &p, int i, TcItem &i
     it.q0 = __ldg(p.query_start + it.b);
     const int nq = __ldg(p.query_start + it.b + 1) - it.q0;
     it.ctx = __ldg(p.seq_lens + it.b);
-    *bad = nq > 0 && (it.ctx < nq || it.ctx > p.W * kBlockTokens ||
-                      (p.lse != nullptr && (it.q0 < 0 || nq > p.num_tokens - it.q0)));
+    *bad = nq > 0 && (it.ctx < nq || it.ctx > p.W * kBlockTokens);
+    if constexpr (MODE != kPlain) *bad = *bad || (nq > 0 && (it.q0 < 0 || nq > p.num_tokens - it.q0));
     if (nq <= 0 || *bad) return false;
     it.rows = nq * p.group;
     const int ntile = (it.rows + kCtaRows - 1) / kCtaRows;
@@ -114,7 +119,7 @@ __device__ __forceinline__ bool tc_item(const PrefillParams &p, int i, TcItem &i
     it.nk0 = (it.first_pos + last0 / p.group + kKeys) / kKeys;
     const int lo1 = it.r_begin + kRows;
     it.nk1 = lo1 < it.rows ? (it.first_pos + (min(it.rows, lo1 + kRows) - 1) / p.group + kKeys) / kKeys : 0;
-    if (SPLIT) {
+    if constexpr (MODE == kSplit) {
         int kb;
         tc_part(max(it.nk0, it.nk1), it.part, p.key_parts, it.ka, kb);
         it.nk0 = max(min(it.nk0, kb) - it.ka, 0);
@@ -131,13 +136,13 @@ __device__ __forceinline__ int tc_item_index(int k, int c, int n) {
 }
 
 // Next valid item of this CTA at or after round k; returns its round or -1.
-template <bool SPLIT>
+template <int MODE>
 __device__ __forceinline__ int tc_next_item(const PrefillParams &p, int k, TcItem &it) {
     for (;; ++k) {
         const int i = tc_item_index(k, blockIdx.x, gridDim.x);
         if (i >= p.items) return -1;
         bool bad;
-        if (tc_item<SPLIT>(p, i, it, &bad)) return k;
+        if (tc_item<MODE>(p, i, it, &bad)) return k;
     }
 }
 
@@ -150,9 +155,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
 // barrier's phase runs on across items, and a dedicated warp fetches the next
 // item's Q rows (cp.async) as soon as the current item's last S product of
 // that Q tile is done.
-// SPLIT (few items, long contexts): a unit is a range of an item's keys, and
-// its rows' unnormalised sums and (max, sum) go to the workspace.
-template <int D, bool SPLIT>
+// kSplit: a unit is a range of an item's keys, and its rows' unnormalised sums
+// and (max, sum) go to the workspace.
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv, const PrefillParams p) {
@@ -215,15 +220,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t policy = l2_policy_evict_normal();
             int gk = 0, gv = 0;  // K / V tiles loaded so far (ring position and phase)
             TcItem it, nx;
-            for (int k = tc_next_item<SPLIT>(p, 0, it); k >= 0 && !*abort_flag; it = nx) {
-                const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
+            for (int k = tc_next_item<MODE>(p, 0, it); k >= 0 && !*abort_flag; it = nx) {
+                const int kn = tc_next_item<MODE>(p, k + 1, nx);
                 const int32_t *trow = p.block_tables + static_cast<size_t>(it.b) * p.W;
                 const int nk = max(it.nk0, it.nk1);
                 for (int j = 0; j < nk && !*abort_flag; ++j) {
                     int y[kKeys / kBlockTokens];  // tensor-map rows of the tile's blocks
 #pragma unroll
                     for (int i = 0; i < kKeys / kBlockTokens; ++i) {
-                        const int blk = (it.ka + j) * (kKeys / kBlockTokens) + i;
+                        const int blk = (MODE == kSplit ? it.ka + j : j) * (kKeys / kBlockTokens) + i;
                         long long yy = p.num_blocks * p.Hkv * kBlockTokens;  // past the tensor: zeros
                         if (blk < it.nblk_seq) {
                             const int32_t phys = __ldg(trow + blk);
@@ -277,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0;; ++k) {
                 const int i = tc_item_index(k, blockIdx.x, gridDim.x);
                 if (i >= p.items) break;
-                const int item = SPLIT ? i / p.key_parts : i;
+                const int item = MODE == kSplit ? i / p.key_parts : i;
                 if (item < p.Hkv * p.B && item % p.Hkv == 0) {
                     TcItem bad_it;
                     bool bad;
-                    tc_item<SPLIT>(p, i, bad_it, &bad);
+                    tc_item<MODE>(p, i, bad_it, &bad);
                     if (bad) flag(p.err, PKV_DEV_ERR_BAD_LEN);
                 }
             }
@@ -330,10 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ns[kTiles] = {0, 0};  // S products per Q tile (s_full / p_full phases)
         int n_it = 0;            // items done (q_full / o_done / o_free phases)
         TcItem it, nx;
-        int k = tc_next_item<SPLIT>(p, 0, it);
+        int k = tc_next_item<MODE>(p, 0, it);
         for (; k >= 0 && ok; it = nx, ++n_it) {
             // the next item's parameters are read now, off the item boundary
-            const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
+            const int kn = tc_next_item<MODE>(p, k + 1, nx);
             const int nk_t[kTiles] = {it.nk0, it.nk1};
             const int nk = max(it.nk0, it.nk1);
             wait(k_full(gk % KS), static_cast<uint32_t>((gk / KS) & 1));
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int sv = gv % VS;
                 wait(v_full(sv), static_cast<uint32_t>((gv / VS) & 1));
                 // V rows of slots at or past the sequence end may hold anything: zero them
-                const int k_lo = (it.ka + j) * kKeys;
+                const int k_lo = (MODE == kSplit ? it.ka + j : j) * kKeys;
                 if (ok && k_lo + kKeys > it.ctx && k_lo < it.nblk_seq * kBlockTokens) {
                     const int z0 = max(it.ctx - k_lo, 0), z1 = min(it.nblk_seq * kBlockTokens - k_lo, kKeys);
                     uint8_t *vbase = smem + Geo::kV + sv * Geo::kKVBytes;
@@ -423,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int n_it = 0;
         TcItem it, nx;
-        for (int k = tc_next_item<SPLIT>(p, 0, it); k >= 0 && ok; it = nx, ++n_it) {
-            const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
+        for (int k = tc_next_item<MODE>(p, 0, it); k >= 0 && ok; it = nx, ++n_it) {
+            const int kn = tc_next_item<MODE>(p, k + 1, nx);
             {
                 if (n_it > 0 && (!mbar_wait(q_free(x), static_cast<uint32_t>((n_it - 1) & 1), kWaitLimitNs) ||
                                  *abort_flag)) {
@@ -470,9 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ns = 0;    // S products seen (s_full / p_full phases)
         int n_it = 0;  // items done (o_done phases)
         TcItem it, nx;  // the current and the next item
-        int k = tc_next_item<SPLIT>(p, 0, it);
+        int k = tc_next_item<MODE>(p, 0, it);
         while (k >= 0 && ok) {
-            const int kn = tc_next_item<SPLIT>(p, k + 1, nx);
+            const int kn = tc_next_item<MODE>(p, k + 1, nx);
             const int r = it.r_begin + tile * kRows + t;
             const int row_pos = r < it.rows ? it.first_pos + r / G : -1;
             const int my_nk = tile == 0 ? it.nk0 : it.nk1;
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Two passes over S in TMEM, 64 columns at a time, so that a row
                 // never sits in registers whole (twelve warps leave 170 registers
                 // a thread): the row max first, then exp2 and P.
-                const int k0 = (it.ka + j) * kKeys;
+                const int k0 = (MODE == kSplit ? it.ka + j : j) * kKeys;
                 const bool masked = __any_sync(0xffffffffu, k0 + kKeys - 1 > row_pos);
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1  // one half's 64 registers live at a time
@@ -597,9 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 k = kn;
                 continue;
             }
-            if constexpr (SPLIT) {  // this part's unnormalised row and (max, sum)
+            if constexpr (MODE == kSplit) {  // this part's unnormalised row and (max, sum)
                 const size_t row = (static_cast<size_t>(it.part) * p.num_tokens + it.q0 + r / G) * p.Hq + it.kvh * G + r % G;
-                const bool live = row_pos >= 0 && it.q0 >= 0 && it.q0 + r / G < p.num_tokens;
+                const bool live = row_pos >= 0;
 #pragma unroll
                 for (int h = 0; h < D / 32; ++h) {
                     uint32_t o[32];
@@ -622,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O row, normalised, packed to bf16 and stored 64 columns at a
             // time; then O_x is handed back
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-            if (p.lse != nullptr && row_pos >= 0 && it.q0 >= 0 && it.q0 + r / G < p.num_tokens)
+            if (MODE == kLse && row_pos >= 0)
                 p.lse[(static_cast<size_t>(it.kvh) * p.num_tokens + it.q0) * G + r] = m_run + log2f(l_run);
             uint4 *dst = reinterpret_cast<uint4 *>(out_row);
 #pragma unroll
@@ -714,22 +719,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
         p.lse[(static_cast<size_t>(kvh) * p.num_tokens + q0) * p.group + r] = M + log2f(L);
 }
 
-template <int D, bool SPLIT>
+template <int D, int MODE>
 cudaError_t launch_prefill_tc_d(const CUtensorMap &tmk, const CUtensorMap &tmv, PrefillParams p,
                                 int max_query_len, int num_sms, cudaStream_t stream) {
     constexpr int kSmem = TcGeometry<D>::kSmemBytes;
-    auto kern = paged_prefill_tc_kernel<D, SPLIT>;
+    auto kern = paged_prefill_tc_kernel<D, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(max_query_len) * p.group;
-    const long long items = (rows + kCtaRows - 1) / kCtaRows * p.Hkv * p.B * (SPLIT ? p.key_parts : 1);
+    const long long items = (rows + kCtaRows - 1) / kCtaRows * p.Hkv * p.B * (MODE == kSplit ? p.key_parts : 1);
     if (items == 0) return cudaSuccess;
     if (items > 0x7FFFFFFFLL - 2LL * num_sms) return cudaErrorInvalidValue;
     p.items = static_cast<int>(items);
     const unsigned grid = static_cast<unsigned>(std::min<long long>(items, num_sms));
     kern<<<grid, kThreads, kSmem, stream>>>(tmk, tmv, p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !SPLIT) return e;
+    if (e != cudaSuccess || MODE != kSplit) return e;
     const long long join_rows = static_cast<long long>(max_query_len) * p.Hq;
     const long long ctas = (join_rows + kJoinWarps - 1) / kJoinWarps;
     if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
@@ -742,13 +747,15 @@ cudaError_t launch_prefill_tc_d(const CUtensorMap &tmk, const CUtensorMap &tmv, 
 
 cudaError_t launch_prefill_tc(const CUtensorMap &tmk, const CUtensorMap &tmv, const PrefillParams &p,
                               int head_dim, int max_query_len, int num_sms, cudaStream_t stream) {
-    if (p.key_parts > 1) {
-        if (head_dim == 128) return launch_prefill_tc_d<128, true>(tmk, tmv, p, max_query_len, num_sms, stream);
-        if (head_dim == 64) return launch_prefill_tc_d<64, true>(tmk, tmv, p, max_query_len, num_sms, stream);
-        return cudaErrorInvalidValue;
-    }
-    if (head_dim == 128) return launch_prefill_tc_d<128, false>(tmk, tmv, p, max_query_len, num_sms, stream);
-    if (head_dim == 64) return launch_prefill_tc_d<64, false>(tmk, tmv, p, max_query_len, num_sms, stream);
+    const int mode = p.key_parts > 1 ? kSplit : p.lse != nullptr ? kLse : kPlain;
+    const auto run = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if (mode == kSplit) return launch_prefill_tc_d<D, kSplit>(tmk, tmv, p, max_query_len, num_sms, stream);
+        if (mode == kLse) return launch_prefill_tc_d<D, kLse>(tmk, tmv, p, max_query_len, num_sms, stream);
+        return launch_prefill_tc_d<D, kPlain>(tmk, tmv, p, max_query_len, num_sms, stream);
+    };
+    if (head_dim == 128) return run(std::integral_constant<int, 128>{});
+    if (head_dim == 64) return run(std::integral_constant<int, 64>{});
     return cudaErrorInvalidValue;
 }
 
