@@ -175,7 +175,7 @@ def _marshalled(symbol, names) -> int:
     return len(_MARSHALLED) - 1
 
 
-_ROPE = _marshalled("pkv_rope_kv_write", "q_out:b q:b k:b v:b . . . . k_cache:b v_cache:b slot_mapping:l "
+_ROPE = _marshalled("pkv_rope_kv_write", "q_out:r q:r k:r v:r . . . . k_cache:b v_cache:b slot_mapping:l "
                     "positions:i . . cos_sin:f . . . . . . . . err:i")
 _DECODE = _marshalled("pkv_paged_attention_decode_scored", "out:b q:b k_new:b v_new:b k_cache:b v_cache:b "
                       "block_tables:i . seq_lens:i . . . . . . scores_in:f scores_out:f . . . . . err:i")
@@ -190,7 +190,9 @@ def _bad_argument(which, i, t):
     import torch
 
     name, letter = _MARSHALLED[which][2][i].split(":")
-    _dev_tensor(t, dict(b=torch.bfloat16, i=torch.int32, l=torch.int64, f=torch.float32)[letter], name)
+    if letter == "r" and isinstance(t, torch.Tensor):  # rows of its own stride
+        t = t[:0].contiguous()
+    _dev_tensor(t, dict(b=torch.bfloat16, r=torch.bfloat16, i=torch.int32, l=torch.int64, f=torch.float32)[letter], name)
     raise ValueError(f"{name}: tensors must be on one device")
 
 
@@ -677,6 +679,7 @@ def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_l
             or seq_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise ValueError("shape mismatch")
     stride = _score_stride(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS)
+    max_query_len, window = int(max_query_len), int(window)
     dev = q.get_device()
     wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else _prefill_scored_bytes(
         dev, T, B, max_query_len, hq, hkv, d, W, window))

@@ -237,7 +237,7 @@ def test_marshalled_arguments_are_the_headers():
             assert (n == ".") == (c in "sp")
             if n != ".":
                 assert arg.endswith("*" + dict(tables="x").get(n.split(":")[0], n.split(":")[0])) or n.startswith("err")
-                assert n.split(":")[1] == dict(r="b").get(c.lower(), c.lower())
+                assert n.split(":")[1] == c.lower()
 
 
 def test_marshal_refuses_what_it_cannot_convert():
