@@ -564,7 +564,7 @@ def rope_kv_write(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos
             or positions.shape != ((T,) if positions.ndim == 1 else (axes, T)):
         raise ValueError("shape mismatch")
     if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
+        pair_axis = bytes(list(pair_axis))  # an array's items, not its memory; no int
         if len(pair_axis) != rot // 2:
             raise ValueError("pair_axis: one axis for each of the rot / 2 pairs")
     qos, qs = _token_stride(q_out, "q_out", hq, d), _token_stride(q, "q", hq, d)
@@ -594,7 +594,7 @@ def decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, m
 
 
 def _score_stride(scores_in, scores_out, B, hkv, tokens) -> int:
-    stride = scores_out.shape[-1]
+    stride = scores_out.shape[-1] if scores_out.ndim else 0
     rows = (B, hkv, stride)
     if scores_out.shape != rows or stride < tokens or (scores_in is not None and scores_in.shape != rows):
         raise ValueError("scores: [B, Hkv, at least the table's tokens], in and out alike")

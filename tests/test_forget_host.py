@@ -202,6 +202,33 @@ def test_binding_refuses_what_does_not_fit():
         pkv.evict_tokens(c, c, i.view(2, 1), i, i.view(2, 1), i, s, s, torch.zeros(2, 4, 8, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("axes,error", [
+    (32, TypeError),                                    # a number is not 32 zeros
+    (np.zeros(4, dtype=np.int64), "one axis"),          # 4 items, though 32 bytes
+    (np.zeros(32, dtype=np.int64), "CUDA"),             # 32 items: refused for the host tensors only
+    ([-1] * 32, ValueError), ([256] * 32, ValueError), ([0.0] * 32, TypeError),
+])
+def test_pair_axis_is_a_sequence_of_ints(axes, error):
+    import torch
+
+    t = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    c = torch.zeros(4, 4, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    kind, text = (ValueError, error) if isinstance(error, str) else (error, None)
+    with pytest.raises(kind, match=text):
+        pkv.rope_kv_write(t, t, t, t, c, c, i.long(), i, torch.zeros(8, 64), pair_axis=axes)
+
+
+def test_scores_without_dimensions_are_refused():
+    import torch
+
+    t = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    c = torch.zeros(4, 4, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="scores"):
+        pkv.paged_attention_decode_scored(t, t, c, c, i.view(2, 1), i, 1.0, 4, torch.zeros(()))
+
+
 def test_rope_table_is_the_cosines_and_sines_of_the_positions():
     import torch
 
