@@ -133,6 +133,10 @@ __device__ __forceinline__ void prefix_unit_tc(const CUtensorMap &tmk, const CUt
     __syncthreads();  // barriers, rows[], keep bits and the TMEM base
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
+    // The merge's CTAs may take their places; they wait for this grid.  Not before
+    // the allocation above: one of them, holding the right to allocate while it
+    // waits, could keep this CTA from its columns for good.
+    pdl_launch_dependents();
     const uint64_t keep = static_cast<uint64_t>(keep_slot[0]) | (static_cast<uint64_t>(keep_slot[1]) << 32);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);  // this thread's lane
     const uint64_t policy = l2_policy_evict_first();
@@ -454,7 +458,7 @@ template <int D, bool MMA>
 __global__ void __launch_bounds__(kPrefixWarps * 32, 3)  // three CTAs per SM, as the suffix units need
     cascade_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const PrefixParams pp, const DecodeParams dp, int n_pre) {
-    pdl_launch_dependents();
+    // (dependents may start once the units have: prefix_unit_tc, decode_unit)
     int id = blockIdx.x;
     const int stride = n_pre > 0 ? max(1, static_cast<int>(gridDim.x) / 8 / n_pre) : 1;
     if (n_pre > 0 && id % stride == 0 && id / stride < n_pre) {

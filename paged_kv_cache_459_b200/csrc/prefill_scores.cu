@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.pp.group;
     const int rows = p.tile_tokens * G;  // rows a Q box fills
-    pdl_launch_dependents();  // the join's CTAs may take their places; they wait for this grid
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -228,6 +227,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
+    // The join's CTAs (or the next call's) may take their places; they wait for
+    // this grid.  Not before the allocation above: one of them, holding the right
+    // to allocate while it waits, could keep this CTA from its columns for good.
+    pdl_launch_dependents();
 
     if (warp == kProducerWarp) {
         if (lane == 0) {

@@ -65,7 +65,9 @@ __device__ __forceinline__ void fence_after() {
 // follow in the same CTA).  A CTA keeps that right until it gives it up or
 // exits, and a later CTA's allocation on the same SM can wait for it
 // (measured: the cascade step took twice as long until its CTAs that never
-// allocate gave the right up at entry).
+// allocate gave the right up at entry).  So a kernel that allocates lets its
+// dependents launch only once it holds its columns: a dependent's CTA that kept
+// the right would wait for this grid, and this grid's allocation for it.
 __device__ __forceinline__ void relinquish() {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }

@@ -1,0 +1,54 @@
+"""Rules of kernels that overlap on a stream (programmatic dependent launches),
+checked on the sources, without a GPU."""
+import pathlib
+import re
+
+import pytest
+
+ROOT = pathlib.Path(__file__).resolve().parents[1]
+CSRC = ROOT / "paged_kv_cache_459_b200" / "csrc"
+SOURCES = sorted(p for p in CSRC.iterdir() if p.suffix in (".cu", ".cuh"))
+
+
+def _code(path):
+    text = re.sub(r"/\*.*?\*/", "", path.read_text(), flags=re.S)
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def _functions(code):
+    """{name: body} of the device functions and kernels of a file."""
+    found = {}
+    code = re.sub(r"__launch_bounds__\([^()]*\)", "", code)
+    for m in re.finditer(r"(?:__global__|__device__)[^;{}]*?\b(\w+)\((?=[^;{}]*\)\s*(?:const\s*)?\{)", code):
+        start = code.index("{", m.end())
+        depth, i = 1, start + 1
+        while depth:
+            depth += {"{": 1, "}": -1}.get(code[i], 0)
+            i += 1
+        found[m.group(1)] = code[start:i]
+    return found
+
+
+def test_the_functions_are_found():
+    assert {"prefill_scores_kernel", "prefill_scores_join_kernel"} <= set(_functions(_code(CSRC / "prefill_scores.cu")))
+    assert {"cascade_kernel", "prefix_unit_tc"} <= set(_functions(_code(CSRC / "decode_prefix.cu")))
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=lambda p: p.name)
+def test_dependents_start_only_after_tensor_memory_is_allocated(path):
+    """A block holds the right to allocate tensor memory until it gives it up or exits, and a
+    dependent's block waits for the whole grid before it does either: started on an SM whose
+    block has not allocated yet, the two would wait for each other.  So a kernel lets
+    dependents start behind its allocation and the barrier that follows it."""
+    if path.name == "tcgen05.cuh":
+        return
+    functions = _functions(_code(path))
+    allocating = {name for name, body in functions.items() if "tc::alloc<" in body}
+    for name, body in functions.items():
+        starts = [m.start() for m in re.finditer(r"\bpdl_launch_dependents\(\)", body)]
+        if name in allocating:
+            done = body.index("__syncthreads()", body.index("tc::alloc<"))
+            assert all(at > done for at in starts), name
+        for callee in allocating - {name}:
+            for call in re.finditer(r"\b%s\s*<" % callee, body):
+                assert all(at > call.start() for at in starts), f"{name} before {callee}"
