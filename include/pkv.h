@@ -6,15 +6,18 @@
  * and every call is asynchronous on the caller's CUDA stream (`stream` is a
  * cudaStream_t passed as void*; NULL = the legacy default stream).
  *
- * Stream order: the decode kernels are programmatic dependent launches, so a
- * call's grid can be resident while the kernel before it on the stream still
- * runs.  Every read of q, the new tokens, the caches and the workspace, and
- * every write, waits for that kernel to finish.  The decode and shared-
+ * Stream order: the decode kernels, the rotary write's and the eviction's are
+ * programmatic dependent launches, so a call's grid can be resident while the
+ * kernel before it on the stream still runs.  Every read of q, the new tokens,
+ * positions, slots, scores, the caches and the workspace, and every write,
+ * waits for that kernel to finish.  The decode, scored decode and shared-
  * prefix calls may read seq_lens, block_tables and prefix_blocks before that
- * wait, so the kernel right before such a call must not write those arrays
- * after it lets dependents launch early (griddepcontrol.launch_dependents).
- * Kernels that never do that are fine, as are copies and memsets; none of
- * this library's kernels writes them.
+ * wait, so a kernel that lets dependents launch early
+ * (griddepcontrol.launch_dependents) must not write those arrays unless
+ * something that starts only when all before it is done -- a kernel launched
+ * without programmatic serialization, a copy, a memset -- lies between it and
+ * the call.  Other kernels' writes are always seen; none of this library's
+ * kernels writes them.
  *
  * The method (page titles and sections of the pages this library follows):
  *  - "vLLM 與 PagedAttention：高吞吐推理的關鍵", section 二: the KV cache is cut

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(NW * 32)
     // soon as it is released.
     if (p.order != nullptr) {
         pdl_wait_primary();
-        decode_unit<D, NW, S, MMA, MODE>(tmk, tmv, p, blockIdx.x, blockIdx.y, __ldg(p.order + blockIdx.z));
+        decode_unit<D, NW, S, MMA, MODE>(tmk, tmv, p, blockIdx.x, blockIdx.y, p.order[blockIdx.z]);
     } else {
         decode_unit<D, NW, S, MMA, MODE>(tmk, tmv, p, blockIdx.x, blockIdx.y, static_cast<int>(blockIdx.z),
                                          true);

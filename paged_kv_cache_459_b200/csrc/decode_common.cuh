@@ -113,7 +113,7 @@ struct ScalarHead {
     __device__ __forceinline__ void init(const __nv_bfloat16 *qrow, float scale_log2, int lane) {
         c = lane % CH;
         g = lane / CH;
-        const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(qrow) + c);
+        const uint4 raw = reinterpret_cast<const uint4 *>(qrow)[c];
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -234,8 +234,8 @@ struct GroupHeads {
         const uint32_t *qrow = reinterpret_cast<const uint32_t *>(q0 + static_cast<size_t>(gid) * D);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            qb[ks][0] = ok ? __ldg(qrow + (16 * ks + 2 * tig) / 2) : 0u;
-            qb[ks][1] = ok ? __ldg(qrow + (16 * ks + 8 + 2 * tig) / 2) : 0u;
+            qb[ks][0] = ok ? qrow[(16 * ks + 2 * tig) / 2] : 0u;
+            qb[ks][1] = ok ? qrow[(16 * ks + 8 + 2 * tig) / 2] : 0u;
         }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt)

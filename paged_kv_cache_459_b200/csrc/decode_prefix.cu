@@ -71,10 +71,10 @@ __device__ __forceinline__ void prefix_unit_tc(const CUtensorMap &tmk, const CUt
     constexpr float kRescale = 8.0f;  // log2 units
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
-    const int off = __ldg(p.group_offsets + g);
-    const int members = __ldg(p.group_offsets + g + 1) - off;
+    const int off = p.group_offsets[g];
+    const int members = p.group_offsets[g + 1] - off;
     if (members <= 0) return;
-    const int b0 = __ldg(p.group_seqs + off);
+    const int b0 = p.group_seqs[off];
     if (b0 < 0 || b0 >= p.B) {
         if (t == 0) flag(p.err, PKV_DEV_ERR_BAD_LEN);
         return;
@@ -170,7 +170,7 @@ __device__ __forceinline__ void prefix_unit_tc(const CUtensorMap &tmk, const CUt
         const int r = r0 + t;
         int b = -1, h = 0;
         if (r < R) {
-            const int bb = __ldg(p.group_seqs + off + r / G);
+            const int bb = p.group_seqs[off + r / G];
             if (bb >= 0 && bb < p.B) {
                 b = bb;
                 h = kvh * G + r % G;
@@ -183,7 +183,7 @@ __device__ __forceinline__ void prefix_unit_tc(const CUtensorMap &tmk, const CUt
             uint32_t w[D / 2];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
-                const uint4 v = b >= 0 ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = b >= 0 ? src[i] : make_uint4(0u, 0u, 0u, 0u);
                 w[4 * i] = v.x;
                 w[4 * i + 1] = v.y;
                 w[4 * i + 2] = v.z;

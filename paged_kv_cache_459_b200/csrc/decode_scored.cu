@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(128)
                                const __grid_constant__ CUtensorMap tmv, const DecodeParams p) {
     if (p.order != nullptr) {
         pdl_wait_primary();
-        decode_unit<D, 4, 2, MMA, MODE, true>(tmk, tmv, p, blockIdx.x, blockIdx.y, __ldg(p.order + blockIdx.z));
+        decode_unit<D, 4, 2, MMA, MODE, true>(tmk, tmv, p, blockIdx.x, blockIdx.y, p.order[blockIdx.z]);
     } else {
         decode_unit<D, 4, 2, MMA, MODE, true>(tmk, tmv, p, blockIdx.x, blockIdx.y, static_cast<int>(blockIdx.z), true);
     }
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kAddThreads) score_add_kernel(const DecodePara
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 if (h + e >= heads) break;
-                const float l = __ldg(lse + h + e);
+                const float l = lse[h + e];
 #pragma unroll
                 for (int i = 0; i < kAddTokens; ++i) w[i] += ex2_approx(x[i][e] - l);
             }

@@ -196,8 +196,8 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
         if (phys >= 0 && phys < p.num_blocks) {
             const bool is_v = lane >= D / 8;
             const int e = (lane % (D / 8)) * 8;
-            new_val = __ldg(reinterpret_cast<const uint4 *>(
-                (is_v ? p.v_new : p.k_new) + (static_cast<size_t>(b) * p.Hkv + kvh) * D + e));
+            new_val = *reinterpret_cast<const uint4 *>(
+                (is_v ? p.v_new : p.k_new) + (static_cast<size_t>(b) * p.Hkv + kvh) * D + e);
             new_dst = (is_v ? p.v_cache : p.k_cache) +
                       ((static_cast<size_t>(phys) * p.Hkv + kvh) * kBlockTokens + pos % kBlockTokens) * D + e;
         }

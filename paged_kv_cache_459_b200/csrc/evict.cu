@@ -40,8 +40,8 @@ struct EvictRow {
 };
 __device__ __forceinline__ EvictRow evict_row(const EvictParams &p, int b, bool *bad) {
     EvictRow e;
-    e.len = __ldg(p.seq_lens + b);
-    int keep = __ldg(p.keep_lens + b);
+    e.len = p.seq_lens[b];
+    int keep = p.keep_lens[b];
     const long long cap = static_cast<long long>(p.W) * kBlockTokens;
     const long long new_cap = static_cast<long long>(p.NW) * kBlockTokens;
     *bad = e.len < 0 || e.len > cap || keep < 0;
@@ -92,11 +92,11 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
 __device__ __forceinline__ void load_keys(const float *in, bool vec, int t0, const EvictRow &e, uint32_t (&k)[kPer]) {
     float x[kPer];
     if (vec && t0 + kPer <= e.len) {
-        *reinterpret_cast<float4 *>(x) = __ldg(reinterpret_cast<const float4 *>(in + t0));
-        *reinterpret_cast<float4 *>(x + 4) = __ldg(reinterpret_cast<const float4 *>(in + t0 + 4));
+        *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(in + t0);
+        *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(in + t0 + 4);
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = t0 + i < e.len ? __ldg(in + t0 + i) : 0.f;
+        for (int i = 0; i < kPer; ++i) x[i] = t0 + i < e.len ? in[t0 + i] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -308,9 +308,9 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Evict
     if (i < e.m) {
         const size_t row = static_cast<size_t>(b) * p.Hkv + h;
         const int t = __ldcg(p.kept + row * (static_cast<size_t>(p.NW) * kBlockTokens) + i);
-        const int32_t to = __ldg(p.new_tables + static_cast<size_t>(b) * p.NW + i / kBlockTokens);
-        const int32_t from = __ldg(p.block_tables + static_cast<size_t>(b) * p.W + t / kBlockTokens);
-        p.scores_out[row * p.out_stride + i] = __ldg(p.scores_in + row * p.in_stride + t);
+        const int32_t to = p.new_tables[static_cast<size_t>(b) * p.NW + i / kBlockTokens];
+        const int32_t from = p.block_tables[static_cast<size_t>(b) * p.W + t / kBlockTokens];
+        p.scores_out[row * p.out_stride + i] = p.scores_in[row * p.in_stride + t];
         if (from >= 0 && from < p.num_blocks && to >= 0 && to < p.num_blocks) {
             src = (from * p.Hkv + h) * kBlockTokens + t % kBlockTokens;
             dst = (to * p.Hkv + h) * kBlockTokens + i % kBlockTokens;

@@ -81,7 +81,9 @@ __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Waits until the preceding grid has completed and its writes are visible.
+// Waits until the preceding grid has completed and its writes are visible: to
+// plain loads (and __ldcg), not to the read-only path (__ldg), which is for data
+// that nothing writes while the kernel lives -- lengths, tables, prefix lists.
 __device__ __forceinline__ void pdl_wait_primary() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -95,11 +95,11 @@ __global__ void __launch_bounds__(kRopeThreads)
     // the first rows are on their way while slot, position and then the table's row are read
     load(row0);
 
-    const long long slot = __ldg(p.slots + t);
+    const long long slot = p.slots[t];
     long long pos[8];
     bool ok = true;
     if (p.axes == 1) {
-        const long long q = __ldg(p.positions + t);
+        const long long q = p.positions[t];
         ok = q >= 0 && q < p.max_positions;
 #pragma unroll
         for (int i = 0; i < 8; ++i) pos[i] = q;
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         long long ax[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-            ax[a] = a < p.axes ? __ldg(p.positions + static_cast<long long>(a) * p.T + t) : 0;
+            ax[a] = a < p.axes ? p.positions[static_cast<long long>(a) * p.T + t] : 0;
             ok = ok && ax[a] >= 0 && ax[a] < p.max_positions;
         }
         const uint32_t bits = turned ? (p.axis_bits[item >> 1] >> (16 * (item & 1))) & 0xFFFFu : 0u;
@@ -135,15 +135,15 @@ __global__ void __launch_bounds__(kRopeThreads)
         if (same) {
             const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + pos[0] * p.rot + i0);
             const float4 *srow = reinterpret_cast<const float4 *>(p.cos_sin + pos[0] * p.rot + half + i0);
-            *reinterpret_cast<float4 *>(c) = __ldg(row);
-            *reinterpret_cast<float4 *>(c + 4) = __ldg(row + 1);
-            *reinterpret_cast<float4 *>(s) = __ldg(srow);
-            *reinterpret_cast<float4 *>(s + 4) = __ldg(srow + 1);
+            *reinterpret_cast<float4 *>(c) = row[0];
+            *reinterpret_cast<float4 *>(c + 4) = row[1];
+            *reinterpret_cast<float4 *>(s) = srow[0];
+            *reinterpret_cast<float4 *>(s + 4) = srow[1];
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                c[i] = __ldg(p.cos_sin + pos[i] * p.rot + i0 + i);
-                s[i] = __ldg(p.cos_sin + pos[i] * p.rot + half + i0 + i);
+                c[i] = p.cos_sin[pos[i] * p.rot + i0 + i];
+                s[i] = p.cos_sin[pos[i] * p.rot + half + i0 + i];
             }
         }
     }

@@ -52,3 +52,31 @@ def test_dependents_start_only_after_tensor_memory_is_allocated(path):
         for callee in allocating - {name}:
             for call in re.finditer(r"\b%s\s*<" % callee, body):
                 assert all(at > call.start() for at in starts), f"{name} before {callee}"
+
+
+# What a kernel may read through the read-only path although the kernel before it on the stream may
+# still run: the arrays that include/pkv.h ("Stream order") asks callers not to write from such a kernel.
+HOST_WRITTEN = ("seq_lens", "block_tables", "prefix_blocks", "start_blocks", "query_start", "trow", "row + first")
+
+
+def test_data_of_an_overlapping_kernel_is_not_read_through_the_read_only_path():
+    """ld.global.nc is for data that nothing writes while the kernel lives.  A dependent lives while
+    the grid before it still writes, so after its wait it reads with plain loads or __ldcg: q, scores,
+    log-sum-exps, the order, slots and positions may be that grid's.  (Kernels launched without
+    programmatic serialization, kv_write.cu's, start when all before them are done.)"""
+    seen = 0
+    for path in SOURCES:
+        code = _code(path)
+        if path.name == "kv_write.cu":
+            assert "pdl_" not in code and "launch_dependent" not in code
+            continue
+        for m in re.finditer(r"__ldg\(", code):
+            depth, i = 1, m.end()
+            while depth:
+                depth += {"(": 1, ")": -1}.get(code[i], 0)
+                i += 1
+            arg = code[m.end():i - 1]
+            seen += 1
+            assert any(name in arg for name in HOST_WRITTEN), f"{path.name}: __ldg({arg})"
+        assert "ld.global.nc" not in code, path.name
+    assert seen > 10
