@@ -148,9 +148,10 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
     const uint64_t policy = l2_policy_evict_first();
     const int y_head = kvh * kBlockTokens;
 
+    bool issuer = lane == 0;   // until it gives up
     auto issue = [&](int i) {  // warp-uniform
         const int32_t phys = tw.get(i);
-        if (lane == 0) {
+        if (issuer) {
             const uint32_t bar = bars + 8 * (i % S);
             if (phys >= 0 && phys < p.num_blocks) {
                 const uint32_t dst = smem_u32(ring + (i % S) * G::kStageBytes);
@@ -221,13 +222,17 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
         logits = p.logits + ((static_cast<size_t>(b) * p.Hkv + kvh) * p.chunks + chunk) *
                                 static_cast<size_t>(p.W) * kBlockTokens * p.logit_width;
 
-    int i = 0;
-    for (; i < n_mine; ++i) {
+    // A lane whose wait gives up (for itself: a vote on every wait takes 2 % of
+    // one sequence's decode) waits and issues no more, but walks the loop to its
+    // end with the others, over whatever the stages hold: no lane is left alone
+    // in a shuffle.
+    int stuck = n_mine;  // the block that did not arrive
+    for (int i = 0; i < n_mine; ++i) {
         tw.advance_to(i, lane);
         const int s = i % S;
-        if (!mbar_wait(bars + 8 * s, static_cast<uint32_t>((i / S) & 1), kWaitLimitNs)) {
-            if (lane == 0) flag(p.err, PKV_DEV_ERR_TIMEOUT);
-            break;
+        if (!mbar_wait(bars + 8 * s, static_cast<uint32_t>((i / S) & 1), stuck < n_mine ? 0 : kWaitLimitNs)) {
+            stuck = min(stuck, i);
+            issuer = false;
         }
         const int32_t phys = tw.get(i);
         if (phys >= 0 && phys < p.num_blocks) {
@@ -254,10 +259,11 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmk, const CUtens
             issue(i + S);
         }
     }
-    if (i < n_mine) {
-        // A wait gave up: let the copies still in flight land before the
-        // shared memory is reused or released (again bounded).
-        for (int j = i; j < n_mine && j < i + S; ++j)
+    if (stuck < n_mine) {
+        flag(p.err, PKV_DEV_ERR_TIMEOUT);
+        // let the copies still in flight land before the shared memory is reused
+        // or released (again bounded)
+        for (int j = stuck; j < n_mine && j < stuck + S; ++j)
             mbar_wait(bars + 8 * (j % S), static_cast<uint32_t>((j / S) & 1), kWaitLimitNs);
     }
 

@@ -296,22 +296,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp == kMmaWarp) {
         constexpr uint32_t kId = tc::idesc_bf16(kKeys, kCols, 0);
+        // a lane that gives up walks on with the others, as in the attention kernel
         bool ok = true;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
             if (ok && (!mbar_wait(bar, parity, kWaitLimitNs) || *abort_flag)) {
                 ok = false;
-                if (lane == 0) {
-                    flag(p.pp.err, PKV_DEV_ERR_TIMEOUT);
-                    *abort_flag = 1;
-                }
+                flag(p.pp.err, PKV_DEV_ERR_TIMEOUT);
+                *abort_flag = 1;
             }
         };
         int g = 0, nu = 0;
         ScoreUnit u;
-        for (int k = next_unit(p, 0, u); k >= 0 && ok; k = next_unit(p, k + 1, u)) {
+        for (int k = next_unit(p, 0, u); k >= 0; k = next_unit(p, k + 1, u)) {
             if (u.n == 0) continue;
             wait(k_full, static_cast<uint32_t>(nu & 1));
-            for (int i = 0; i < u.n && ok; ++i, ++g) {
+            for (int i = 0; i < u.n; ++i, ++g) {
                 const int s = g % kQStages, x = g % kSBuffers;
                 wait(q_full(s), static_cast<uint32_t>((g / kQStages) & 1));
                 if (g >= kSBuffers) wait(s_empty(x), static_cast<uint32_t>((g / kSBuffers - 1) & 1));
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int i = 0; i < u.n; ++i, ++g) {
                 const int x = g % kSBuffers;
                 if (g >= kSBuffers &&
-                    (!mbar_wait(s_empty(x), static_cast<uint32_t>((g / kSBuffers - 1) & 1), kWaitLimitNs) || *abort_flag)) {
+                    !mbar_wait_warp(s_empty(x), static_cast<uint32_t>((g / kSBuffers - 1) & 1), kWaitLimitNs, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -400,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float total = 0.f;
             for (int i = 0; i < u.n; ++i, ++g) {
                 const int x = g % kSBuffers;
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full(x), static_cast<uint32_t>((g / kSBuffers) & 1), kWaitLimitNs));
+                ok = mbar_wait_warp(s_full(x), static_cast<uint32_t>((g / kSBuffers) & 1), kWaitLimitNs);
                 if (!ok) break;
                 tc::fence_after();
                 uint32_t sr[2][32];

@@ -320,15 +320,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mma_ts(tmem + Geo::kO + D * x, tmem + kKeys * x + 8 * k,
                         tc::smem_desc(vbase + k * (16 * 128), kKeys * 128, 1024), kIdO, acc || k > 0);
         };
+        // A lane that gives up (for itself: a vote on every wait takes 1.7 % of the
+        // kernel) neither waits nor issues any more, but walks the loops to their
+        // end with the others: no lane is left alone in a __syncwarp.
         bool ok = true;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
-            if (!ok) return;
-            if (!mbar_wait(bar, parity, kWaitLimitNs) || *abort_flag) {
+            if (ok && (!mbar_wait(bar, parity, kWaitLimitNs) || *abort_flag)) {
                 ok = false;
-                if (lane == 0) {
-                    flag(p.err, PKV_DEV_ERR_TIMEOUT);
-                    *abort_flag = 1;
-                }
+                flag(p.err, PKV_DEV_ERR_TIMEOUT);
+                *abort_flag = 1;
             }
         };
         int gk = 0, gv = 0;      // K / V tiles consumed
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n_it = 0;            // items done (q_full / o_done / o_free phases)
         TcItem it, nx;
         int k = tc_next_item<MODE>(p, 0, it);
-        for (; k >= 0 && ok; it = nx, ++n_it) {
+        for (; k >= 0; it = nx, ++n_it) {
             // the next item's parameters are read now, off the item boundary
             const int kn = tc_next_item<MODE>(p, k + 1, nx);
             const int nk_t[kTiles] = {it.nk0, it.nk1};
@@ -356,15 +356,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && lane == 0) tc::commit(k_empty(gk % KS));
             __syncwarp();
             ++gk;
-            for (int j = 0; j < nk && ok; ++j, ++gv) {
+            for (int j = 0; j < nk; ++j, ++gv) {
                 const int sv = gv % VS;
                 wait(v_full(sv), static_cast<uint32_t>((gv / VS) & 1));
                 // V rows of slots at or past the sequence end may hold anything: zero them
                 const int k_lo = (MODE == kSplit ? it.ka + j : j) * kKeys;
-                if (ok && k_lo + kKeys > it.ctx && k_lo < it.nblk_seq * kBlockTokens) {
+                if (k_lo + kKeys > it.ctx && k_lo < it.nblk_seq * kBlockTokens) {
                     const int z0 = max(it.ctx - k_lo, 0), z1 = min(it.nblk_seq * kBlockTokens - k_lo, kKeys);
                     uint8_t *vbase = smem + Geo::kV + sv * Geo::kKVBytes;
-                    for (int idx = lane; idx < (z1 - z0) * Geo::kHalves * 8; idx += 32) {
+                    for (int idx = lane; ok && idx < (z1 - z0) * Geo::kHalves * 8; idx += 32) {
                         const int rr = z0 + idx / (Geo::kHalves * 8), rest = idx % (Geo::kHalves * 8);
                         *reinterpret_cast<uint4 *>(vbase + (rest >> 3) * (kKeys * 128) + rr * 128 +
                                                    ((rest & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -431,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = tc_next_item<MODE>(p, 0, it); k >= 0 && ok; it = nx, ++n_it) {
             const int kn = tc_next_item<MODE>(p, k + 1, nx);
             {
-                if (n_it > 0 && (!mbar_wait(q_free(x), static_cast<uint32_t>((n_it - 1) & 1), kWaitLimitNs) ||
-                                 *abort_flag)) {
+                if (n_it > 0 &&
+                    !mbar_wait_warp(q_free(x), static_cast<uint32_t>((n_it - 1) & 1), kWaitLimitNs, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -486,16 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < my_nk; ++j, ++ns) {
                 // S_x(j) done; it was issued after PV_x(j - 1), so O_x is free too
-                if (!mbar_wait(s_full(tile), static_cast<uint32_t>(ns & 1), kWaitLimitNs) || *abort_flag) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait(s_full(tile), static_cast<uint32_t>(ns & 1), kWaitLimitNs) && !*abort_flag;
                 tc::fence_after();
                 // Two passes over S in TMEM, 64 columns at a time, so that a row
                 // never sits in registers whole (twelve warps leave 170 registers
                 // a thread): the row max first, then exp2 and P.
                 const int k0 = (MODE == kSplit ? it.ka + j : j) * kKeys;
                 const bool masked = __any_sync(0xffffffffu, k0 + kKeys - 1 > row_pos);
+                ok = __all_sync(0xffffffffu, ok);  // the warp gives up as one
+                if (!ok) break;
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1  // one half's 64 registers live at a time
                 for (int h = 0; h < kKeys / 64; ++h) {
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // O_x of this item complete (a tile without rows gets a bare commit)
-            if (!mbar_wait(o_done(tile), static_cast<uint32_t>(n_it & 1), kWaitLimitNs) || *abort_flag) {
+            if (!mbar_wait_warp(o_done(tile), static_cast<uint32_t>(n_it & 1), kWaitLimitNs, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -656,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             it = nx;
             k = kn;
         }
-        if (!ok && t == 0) {
+        if (!ok && lane == 0) {
             flag(p.err, PKV_DEV_ERR_TIMEOUT);
             *abort_flag = 1;
         }

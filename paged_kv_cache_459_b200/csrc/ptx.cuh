@@ -62,6 +62,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// mbar_wait by a whole warp whose lanes go on, or give up, together (also where
+// a lane sees *abort set): a lane that left alone would keep the others in their
+// next vote, shuffle or tensor-memory access for good.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                               const volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns) && !*abort);
+}
+
 // Orders this thread's earlier generic-proxy global-memory writes before later
 // async-proxy (TMA) reads of the same bytes.
 __device__ __forceinline__ void fence_proxy_async_global() {

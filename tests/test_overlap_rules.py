@@ -80,3 +80,50 @@ def test_data_of_an_overlapping_kernel_is_not_read_through_the_read_only_path():
             assert any(name in arg for name in HOST_WRITTEN), f"{path.name}: __ldg({arg})"
         assert "ld.global.nc" not in code, path.name
     assert seen > 10
+
+
+def _without_one_thread_code(code):
+    """The code without what a single thread runs: if (lane == 0) and its like, block or statement."""
+    out, at = [], 0
+    for m in re.finditer(r"\bif \((?:[^()]*&& )?(?:lane|t|threadIdx\.x) == 0\)\s*", code):
+        if m.start() < at:
+            continue
+        out.append(code[at:m.start()])
+        i, depth = m.end(), 0
+        while True:
+            depth += {"{": 1, "(": 1, "}": -1, ")": -1}.get(code[i], 0)
+            if depth == 0 and code[i] in "};":
+                break
+            i += 1
+        at = i + 1
+    return "".join(out) + code[at:]
+
+
+def _statement(code, start):
+    """The statement (with its block) that starts at or holds `start`, from there to its end."""
+    depth, i = 0, start
+    while True:
+        depth += {"{": 1, "}": -1}.get(code[i], 0)
+        if depth < 0 or (depth == 0 and code[i] in ";}"):
+            return code[start:i + 1]
+        i += 1
+
+
+@pytest.mark.parametrize("path", [p for p in SOURCES if p.name != "ptx.cuh"], ids=lambda p: p.name)
+def test_no_lane_leaves_its_warp_over_a_wait(path):
+    """Lanes that timed out, or saw the abort flag, alone must not leave the others in a warp-wide
+    vote, shuffle or tensor-memory access, which would then never end.  A wait that several lanes make
+    is decided by a vote of the warp (mbar_wait_warp) or of the block, or it steers no jump: the lane
+    only remembers it, and leaves loops by a vote or at their natural end."""
+    left = _without_one_thread_code(_code(path))
+    for m in re.finditer(r"\bmbar_wait\(", left):
+        if left[:m.start()].endswith("__syncthreads_or(!"):
+            continue
+        then = _statement(left, m.start())
+        assert not re.search(r"\b(break|return|continue|goto)\b", then), f"{path.name}: {then}"
+    for m in re.finditer(r"warp == kMmaWarp\) \{", left):  # its lanes' `ok` is each lane's own
+        role = _statement(left, m.end() - 1)
+        loops = re.findall(r"\b(?:for|while) \((?:[^()]|\([^()]*\))*\)", role)
+        for loop in loops:
+            assert not re.search(r"\bok\b", loop) or "idx = lane" in loop, f"{path.name}: {loop}"
+        assert "tc::dealloc" in role or not re.search(r"\b(break|return|goto)\b", role), path.name
