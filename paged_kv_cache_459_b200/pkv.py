@@ -638,24 +638,25 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
 def _prefill_scored_bytes(dev, *sizes) -> int:
     import torch
 
-    if dev < 0:
-        return int(_lib.pkv_prefill_scored_workspace_bytes(*sizes))
     with torch.cuda.device(dev):  # the size goes by the device's SMs
         return int(_lib.pkv_prefill_scored_workspace_bytes(*sizes))
 
 
 def prefill_scored_workspace_bytes(num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads,
                                    head_dim, max_blocks_per_seq, window=0, device=None) -> int:
-    """Workspace of paged_attention_prefill_scored for these sizes on a CUDA device (default: the
-    current one)."""
+    """Workspace of paged_attention_prefill_scored for these sizes on a CUDA device (default, and
+    what a device without an index stands for: the current one)."""
     import torch
 
-    if device is not None:
-        dev = torch.device(device).index
-    else:
-        dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    return _prefill_scored_bytes(-1 if dev is None else dev, num_tokens, num_seqs, max_query_len,
-                                 num_heads, num_kv_heads, head_dim, max_blocks_per_seq, window)
+    sizes = (num_tokens, num_seqs, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, window)
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("device must be a CUDA device")
+    if device.index is not None:
+        return _prefill_scored_bytes(device.index, *sizes)
+    if torch.cuda.is_available():
+        return _prefill_scored_bytes(torch.cuda.current_device(), *sizes)
+    return int(_lib.pkv_prefill_scored_workspace_bytes(*sizes))  # no device to remember it for
 
 
 def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, scale,
@@ -681,7 +682,7 @@ def paged_attention_prefill_scored(out, q, k_cache, v_cache, block_tables, seq_l
     stride = _score_stride(scores_in, scores_out, B, hkv, W * BLOCK_TOKENS)
     max_query_len, window = int(max_query_len), int(window)
     dev = q.get_device()
-    wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None else _prefill_scored_bytes(
+    wp, wn, _keep = _scratch(dev, workspace, 0 if workspace is not None or dev < 0 else _prefill_scored_bytes(
         dev, T, B, max_query_len, hq, hkv, d, W, window))
     _run(_PREFILL, dev, out, q, T, k_cache, v_cache, block_tables, W, seq_lens, query_start, B, max_query_len, hq,
          hkv, d, nb, scale, scores_in, scores_out, stride, window, wp, wn, err)

@@ -292,3 +292,26 @@ def test_marshal_refuses_what_it_cannot_convert():
             _marshal.call(pkv._EVICT, address, -1, *a)
     # the same tables before and after: the library's own check answers
     assert _marshal.call(pkv._EVICT, address, -1, *args) == pkv.ERR_INVALID_ARG
+
+
+def test_prefill_workspace_goes_by_the_device_it_is_asked_for(monkeypatch):
+    """A device without an index is the current one, and without a CUDA device nothing is remembered:
+    the size depends on the SMs of whatever device the library then sees."""
+    import torch
+
+    asked = []
+    sizes = (20, 2, 16, 4, 2, 64, 8)
+    host = pkv.prefill_scored_workspace_bytes(*sizes) if not torch.cuda.is_available() else None
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(pkv, "_prefill_scored_bytes", lambda dev, *s: asked.append((dev, s)) or 7)
+    for device in (None, "cuda", torch.device("cuda"), "cuda:1", torch.device("cuda", 2), 5):
+        assert pkv.prefill_scored_workspace_bytes(*sizes, window=4, device=device) == 7
+    assert [d for d, _ in asked] == [3, 3, 3, 1, 2, 5] and all(s == (*sizes, 4) for _, s in asked)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkv.prefill_scored_workspace_bytes(*sizes, device="cpu")
+    monkeypatch.undo()
+    if host is not None:
+        before = pkv._prefill_scored_bytes.cache_info()
+        assert pkv.prefill_scored_workspace_bytes(*sizes) == host > 0
+        assert pkv._prefill_scored_bytes.cache_info() == before
