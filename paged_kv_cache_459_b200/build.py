@@ -1,5 +1,6 @@
-"""Build ``libpkv.so`` in-tree with nvcc for sm_100a (B200), and ``_marshal.so``, the
-argument marshalling of some of the Python binding's calls, with the host compiler.
+"""Build ``libpkv.so`` in-tree with nvcc for sm_100a (B200), and ``_marshal``, the argument
+marshalling of four of the Python binding's calls, with the host compiler (an extension
+module of the interpreter that builds it, under its suffix).
 
     python -m paged_kv_cache_459_b200.build [--force] [--verbose-ptxas]
 
@@ -20,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpkv.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
-MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -46,6 +47,9 @@ def _stale() -> bool:
 
 
 def build_marshal(force: bool = False) -> str:
+    untagged = os.path.join(HERE, "_marshal.so")  # as once built: any interpreter would take it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     deps = [MARSHAL_SRC, os.path.join(ROOT, "include", "pkv.h")]
     if not force and os.path.exists(MARSHAL) \
             and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
@@ -58,13 +62,12 @@ def build_marshal(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    build_marshal(force)
-    if not force and not _stale():
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose_ptxas else []), "-o", tmp, *sources()]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    if force or _stale():
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [NVCC, *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose_ptxas else []), "-o", tmp, *sources()]
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+    build_marshal(force)  # after the library, which the other calls need alone
     return LIB
 
 

@@ -21,14 +21,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "pkv.h")
 
-_MARSHAL_PATH = os.path.join(_HERE, "_marshal.so")
-
-if not os.path.exists(LIB_PATH) or not os.path.exists(_MARSHAL_PATH):
+if not os.path.exists(LIB_PATH):
     raise ImportError(
-        f"{LIB_PATH if not os.path.exists(LIB_PATH) else _MARSHAL_PATH} is missing: build it with `python -m paged_kv_cache_459_b200.build` "
+        f"{LIB_PATH} is missing: build it with `python -m paged_kv_cache_459_b200.build` "
         "(nvcc, sm_100a). There is no CPU fallback.")
-
-from . import _marshal  # noqa: E402
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -166,7 +162,21 @@ def _stream_ptr(device) -> int:
 # The calls that _marshal makes: their tensors' types are checked there (csrc/marshal.c),
 # shapes and sizes here.  For each, its address and the names of its arguments.
 _MARSHALLED = []
-_DTYPES: list = []
+_marshal = None  # imported by the first of these calls: the others do without it
+
+
+def _load_marshal() -> None:
+    global _marshal
+    import torch
+
+    try:
+        from . import _marshal as module
+    except ImportError as e:
+        raise ImportError("the argument marshalling of the rotary write, the scored attention and the eviction is "
+                          "missing for this interpreter: build it with `python -m paged_kv_cache_459_b200.build` "
+                          "(C compiler, Python headers)") from e
+    module.setup(torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8)
+    _marshal = module
 
 
 def _marshalled(symbol, names) -> int:
@@ -200,9 +210,8 @@ def _run(which, dev: int, *args) -> None:
     """A marshalled call on device `dev`'s current stream, with that device current."""
     import torch
 
-    if not _DTYPES:
-        _marshal.setup(torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8)
-        _DTYPES.append(True)
+    if _marshal is None:
+        _load_marshal()
     if dev < 0:  # not a CUDA tensor
         code = -1
     elif dev == torch._C._cuda_getDevice():

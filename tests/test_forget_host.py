@@ -315,3 +315,46 @@ def test_prefill_workspace_goes_by_the_device_it_is_asked_for(monkeypatch):
         before = pkv._prefill_scored_bytes.cache_info()
         assert pkv.prefill_scored_workspace_bytes(*sizes) == host > 0
         assert pkv._prefill_scored_bytes.cache_info() == before
+
+
+def _python(code, **env):
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    return subprocess.run([sys.executable, "-c", code], cwd=root, env={**os.environ, **env}, capture_output=True, text=True)
+
+
+def test_calls_without_marshalled_arguments_need_no_marshal_module():
+    """The package imports, and its older calls answer, where the marshalling module is missing (another
+    interpreter's, no compiler when it was built); the four calls that use it say what to build."""
+    r = _python("""
+import sys
+sys.modules["paged_kv_cache_459_b200._marshal"] = None   # importing it raises ImportError
+from paged_kv_cache_459_b200 import pkv
+a = pkv.BlockAllocator(4)
+a.add_seq(0, 20)
+assert pkv.decode_workspace_bytes(2, 4, 64, 8) > 0 and a.export([0], 2)[1].tolist() == [20]
+import torch
+t = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+c = torch.zeros(4, 4, 16, 64, dtype=torch.bfloat16)
+i = torch.zeros(2, dtype=torch.int32)
+try:
+    pkv.rope_kv_write(t, t, t, t, c, c, i.long(), i, torch.zeros(8, 64))
+except ImportError as e:
+    assert "paged_kv_cache_459_b200.build" in str(e), e
+    print("refused")
+""")
+    assert r.returncode == 0 and r.stdout.split() == ["refused"], r.stderr
+
+
+def test_marshal_module_carries_its_interpreters_suffix():
+    """Another interpreter does not take the file for its own, and builds one beside it."""
+    import sysconfig
+
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert pkv_build.MARSHAL.endswith("_marshal" + suffix)
+    from paged_kv_cache_459_b200 import _marshal
+
+    assert _marshal.__file__ == pkv_build.MARSHAL
