@@ -454,6 +454,15 @@ PKV_API pkv_status pkv_rope_kv_write(void *q_out, const void *q, const void *k, 
  * ------------------------------------------------------------------------ */
 
 /*
+ * A captured call's tables are as wide as its longest sequence may become, and the
+ * three calls below plan by that width (max_blocks_per_seq), not by the lengths:
+ * their grids, and the scored decode's workspace, which holds a float for every
+ * token of every table row and query head (heads of a KV head rounded up to even,
+ * above 8 to a multiple of 8): 256 sequences, 32/8 heads and tables of 131072
+ * tokens make 4.3 GB, whatever the lengths.  Keep tables no wider than needed.
+ */
+
+/*
  * pkv_paged_attention_decode_ex -- or, with k_new and v_new (both or neither),
  * pkv_paged_decode_step -- that also gives
  *   scores_out[b][g][p] = (p < seq_lens[b] - 1 ? scores_in[b][g][p] : 0)
@@ -618,7 +627,8 @@ PKV_API pkv_status pkv_alloc_take_swaps(pkv_alloc *a, int direction, int64_t *gp
  * none (PKV_ERR_OOM when the free blocks do not hold the kept tokens: evict
  * fewer sequences at a time).  Old blocks that other tables hold stay theirs.
  * The eviction must be ordered on the GPU before the next writes into the
- * returned blocks, and after queued copies (pkv_alloc_take_copies). */
+ * returned blocks, and after queued copies and swaps (pkv_alloc_take_copies,
+ * pkv_alloc_take_swaps: a fresh block may be one that a queued swap-out reads). */
 PKV_API pkv_status pkv_alloc_evict(pkv_alloc *a, const int64_t *seq_ids, int n,
                                    const int64_t *keep_tokens);
 

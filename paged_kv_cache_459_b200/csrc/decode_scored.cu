@@ -13,9 +13,11 @@
 // it is in L2 (K and V are loaded evict-first).  (Adding inside the unit when
 // it is done, to save the launch, took the single pass from 223 to 235 us at
 // 256 sequences: 128 threads a CTA wait for L2 where they could stream K and V.)
-// Measured: 256 sequences of 512 to 4096 tokens, 28/4 heads: the units 196 us
-// (183 without scores: their 67 MB of logits), this kernel 18; 8 x 32768, 32/8
-// heads: 163 + the merge + 10.
+// Measured: 256 sequences of 512 to 4096 tokens, 28/4 heads: the units 194 us (183
+// without scores: the logits of 609 thousand tokens and 4 KV heads, 68 MB, 78 as
+// stored with 7 heads padded to 8), this kernel 18; 8 x 32768, 32/8 heads: 162 + the
+// merge's 7 + 10.  The workspace has a place for every token of every table, and the
+// grid of this kernel a CTA for every 512 of them: both go by the tables' width.
 #include "decode_unit.cuh"
 
 namespace pkv {

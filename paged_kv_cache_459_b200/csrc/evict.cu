@@ -16,7 +16,7 @@
 // kept positions: every key above the threshold and the first of those equal
 // to it.  No sort, and the result does not depend on the order of any atomic.
 // evict_copy_kernel: the rows and their scores; bound by HBM (each kept row
-// read and written once): 302 MB in 51 us, 268 MB in 42 us (5.9 and 6.4 TB/s).
+// read and written once): 302 MB in 51 us, 268 MB in 42 us (5.9 and 6.3 TB/s).
 #include <algorithm>
 
 #include "decode_common.cuh"
@@ -106,9 +106,10 @@ __device__ __forceinline__ void load_keys(const float *in, bool vec, int t0, con
 // A few microseconds of barriers and first executions: 8 keys a thread stay in
 // registers (a round; longer slices read theirs again each pass).  For 256 rows
 // of about 2300 scores it takes 10 us, with 16 keys unrolled 17, with the keys
-// in shared memory 14; for 64 rows of 32768, four CTAs a row take 22 us (with
-// 16 keys 23.5, though none is read twice), two 32 and eight 27 (their five
-// cluster barriers), one with all keys in shared memory 38.
+// in shared memory 14; for 64 rows of 32768, four CTAs a row take 23 us (22 when
+// the other figures here were taken: with 16 keys 23.5, though none is read twice,
+// two CTAs 32 and eight 27 -- their five cluster barriers --, one with all keys in
+// shared memory 38).
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, int slices) {
     pdl_launch_dependents();
     // A pass counts into kCopies histograms, a lane into its own (scores share few

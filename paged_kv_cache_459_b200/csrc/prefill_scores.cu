@@ -16,12 +16,13 @@
 // share an SM, so that the products of one tile run behind the exponentials
 // of another.  The exponentials bound it: 128 x 128 of them take the
 // special-function unit 1024 cycles, the tile's products 512.  Measured: 4 x
-// 2048 tokens, 32 heads of 128, every query counted: 120 us (0.57 PFLOP/s); the
-// two CTAs' warps take a tile pair in ~3100 cycles of the 2048 the unit needs
-// (a warp alone 2300 for its 128 columns: the products' operand reads and the
-// -lse reads share shared memory, 300 of them).  Eight exponential warps a CTA,
-// a barrier a tile instead of the -lse warp, and a hand-ordered loop measured
-// the same or slower (329, 350 and 329 us a call against 323).
+// 2048 tokens, 32 heads of 128, every query counted: 115 us (0.60 PFLOP/s).  Taken
+// when it was 120: the two CTAs' warps take a tile pair in ~3100 cycles of the
+// 2048 the unit needs (a warp alone 2300 for its 128 columns: the products'
+// operand reads and the -lse reads share shared memory, 300 of them); eight
+// exponential warps a CTA, a barrier a tile instead of the -lse warp, and a
+// hand-ordered loop measured the same or slower (329, 350 and 329 us a call
+// against 323).
 // Few units (few sequences, short contexts): each unit's queries are cut into
 // `splits` ranges whose sums a second kernel adds in order.
 #include <algorithm>

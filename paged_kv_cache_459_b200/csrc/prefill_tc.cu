@@ -320,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mma_ts(tmem + Geo::kO + D * x, tmem + kKeys * x + 8 * k,
                         tc::smem_desc(vbase + k * (16 * 128), kKeys * 128, 1024), kIdO, acc || k > 0);
         };
-        // A lane that gives up (for itself: a vote on every wait takes 1.7 % of the
-        // kernel) neither waits nor issues any more, but walks the loops to their
-        // end with the others: no lane is left alone in a __syncwarp.
+        // A lane that gives up (for itself: with a vote on every wait 652 TFLOP/s
+        // instead of 694) neither waits nor issues any more, but walks the loops to
+        // their end with the others: no lane is left alone in a __syncwarp.
         bool ok = true;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
             if (ok && (!mbar_wait(bar, parity, kWaitLimitNs) || *abort_flag)) {
@@ -761,8 +761,8 @@ cudaError_t launch_prefill_tc(const CUtensorMap &tmk, const CUtensorMap &tmv, co
 int prefill_key_parts(int B, int Hq, int Hkv, int head_dim, int W, int max_query_len, int num_tokens, int num_sms) {
     // Only where the items do not give every SM one (30 new tokens after 10000, 2
     // KV heads: 46 us a scored call against 235 uncut; one token after 12000, 8
-    // heads: 68 against 306).  With more, cutting the last, partly filled round
-    // gained nothing (224 items: 609 us against 611; 256: 217 against 213).
+    // heads: 68 against 306).  With more, cutting every item does not gain: 224
+    // items on 148 SMs in 2, 3 or 5 parts 642, 585 and 606 us, uncut 584.
     // Time in steps of one 128-key tile (two Q tiles against it): rounds of units
     // over the SMs, each unit its steps and kUnit more (Q, the last step's mask,
     // the epilogue), and the partials written and read.

@@ -10,10 +10,11 @@
 // launch for decode steps.  A lane owns one item of a row -- two 16-byte
 // vectors that hold 8 whole pairs -- in every row its warp takes, so the
 // token's 8 cosines and 8 sines are read once and stay in registers while the
-// warp walks the token's q, k and v rows, kBatch rows' loads in flight (4: 24.9
-// us where 3 takes 24.0; a warp for every kBatch rows instead of a whole token:
-// 33.5).  Measured: 7411 tokens, 28/4 heads, 3 axes, 24.8 us (5.7 TB/s); 32768
-// tokens, 32/8 heads of 64, half rotated, 64.1 us (6.35 TB/s); 64 tokens 2.7 us.
+// warp walks the token's q, k and v rows, kBatch rows' loads in flight.  Measured,
+// calls back to back: 7411 tokens, 28/4 heads, 3 axes, 24.7 us (5.7 TB/s; 25.5 with
+// kBatch 2, 25.7 with 4, 30.3 with a warp for every kBatch rows instead of a whole
+// token); 32768 tokens, 32/8 heads of 64, half rotated, 64.0 us (6.36 TB/s; 64.0,
+// 65.1 and 63.6); 64 tokens 2.7 us.
 #include "decode_common.cuh"
 
 namespace pkv {
